@@ -84,7 +84,7 @@ extern "C" {
 typedef enum {
   SAGE_OK = 0,
   SAGE_ERR_INVALID_ARG = 1, /* null/misaligned pointer, negative size, short workspace,
-                               (from sage_fp4_get_device_error) a bad sequence table */
+                               (from sage_fp4_get_device_error) a bad sequence or page table */
   SAGE_ERR_UNSUPPORTED = 2, /* D not in {64, 128}, or a size beyond the 32-bit indexing limits */
   SAGE_ERR_CUDA = 3,        /* a CUDA runtime/driver call or launch failed */
   SAGE_ERR_TIMEOUT = 4,     /* a bounded wait inside a kernel ran out (see above) */
@@ -343,6 +343,129 @@ int sage_fp4_bounds_checked(void);
  * Applies to launches made after the call.
  */
 sage_status_t sage_fp4_set_wait_timeout_ns(uint64_t ns);
+
+/* ------------------------------------------------------- paged key/value cache ---- */
+
+/*
+ * Generating tokens with the attention above needs four more operations: the norm and
+ * rotation of query and key heads, a cache that holds keys and values page by page, reading
+ * it back as dense tensors, and attention of one new token per sequence over it.
+ *
+ * Norm and rotation of one head x (D channels), in binary32 with one rounding at the end:
+ *   y = x * w / sqrt(mean(x^2) + eps)                 (with weights w; the mean in binary64)
+ *   (y_i, y_j) -> (y_i c - y_j s, y_j c + y_i s)      (with a table) for the R / 2 pairs of
+ *   the first R = rotary_dim channels: j = i + R/2, or (2i, 2i + 1) when interleaved;
+ *   c = rope[pos * R + pair], s = rope[pos * R + R/2 + pair].
+ */
+typedef struct {
+  const void* q_weight;   /* [D] norm weights of the query heads, or NULL: no norm */
+  const void* k_weight;   /* [D] norm weights of the key heads, or NULL: no norm */
+  int weight_f32;         /* 0: weights have the tensors' dtype; else float32 */
+  float eps;              /* >= 0 */
+  const float* rope;      /* [rope_len, rotary_dim]: cosines, then sines; or NULL: no rotation */
+  int rope_len;           /* positions in the table */
+  int rotary_dim;         /* a multiple of 32, at most D (ignored without a table) */
+  int interleaved;
+} sage_fp4_rope_t;
+
+/* Rows to norm and rotate: element (sequence b, head h, token n) of x at
+ * x + b*x_stride[0] + h*x_stride[1] + n*x_stride[2] elements, of y likewise. y may be x (with
+ * the same strides); otherwise the two must not overlap. Strides are non-negative multiples of 8. */
+typedef struct {
+  const void* x;
+  void* y;
+  int heads;              /* 0: no rows, everything else ignored */
+  int64_t x_stride[3], y_stride[3];
+} sage_fp4_rows_t;
+
+/*
+ * Norm and rotation of query and key heads in one pass over them. B sequences of N tokens;
+ * positions: device [B * N] int32 (token b*N + n), or NULL: position n. A token whose
+ * position is outside the table leaves its output rows as they were and sets the device
+ * error word (sage_fp4_get_device_error returns SAGE_ERR_INVALID_ARG).
+ */
+sage_status_t sage_fp4_norm_rope(const sage_fp4_rows_t* q, const sage_fp4_rows_t* k, int B, int N, int D,
+                                 sage_dtype_t dtype, const sage_fp4_rope_t* rope, const int32_t* positions,
+                                 void* stream);
+
+typedef enum {
+  SAGE_CACHE_16BIT = 0,  /* elements of the cache's dtype */
+  SAGE_CACHE_FP4 = 1     /* E2M1 codes, two per byte (even channel low), and one E4M3 scale per 16
+                            channels: scale = E4M3(absmax / 6), code = E2M1(x / scale), the rule of
+                            step 2 on single tokens. Elements that are not finite saturate (NaN: to
+                            the largest value) */
+} sage_cache_format_t;
+
+/*
+ * A paged cache of one layer: num_pages pages of page_size token slots. Row (page, head, slot)
+ * of K starts at element page*k_stride[0] + head*k_stride[1] + slot*k_stride[2] (V likewise):
+ * D 16-bit elements, or D/2 bytes of codes at half that offset in k with D/16 scale bytes at
+ * 1/16 of it in k_sf. Strides are non-negative, multiples of 8 (FP4: of D); rows must not
+ * overlap. Each of K and V may reach 2^32 units of 16 bytes.
+ */
+typedef struct {
+  void *k, *v;                       /* 16-byte aligned */
+  uint8_t *k_sf, *v_sf;              /* FP4 only (8-byte aligned) */
+  int64_t k_stride[3], v_stride[3];
+  int num_pages, page_size, Hkv, D;  /* D: 64 or 128 */
+  sage_dtype_t dtype;                /* of every dense tensor that goes in or out */
+  sage_cache_format_t format;
+} sage_fp4_cache_t;
+
+/*
+ * Sequences in a cache. Position p of sequence b is slot p % page_size of page
+ * page_table[b * table_stride + p / page_size]. seq_lens[b] counts the tokens of sequence b,
+ * in append the new ones included. The tokens a call appends or gathers are the last
+ * cu_seqlens[b+1] - cu_seqlens[b] of each sequence, rows cu_seqlens[b] .. of the dense tensors
+ * (NULL: the last one of each, row b). These tables live on the device and are checked there:
+ * a length below 0 or beyond table_width * page_size, a token at a negative position, or a page
+ * outside the cache sets the device error word (sage_fp4_get_device_error returns
+ * SAGE_ERR_INVALID_ARG) and is never followed: append and gather leave the token out,
+ * attention clamps the length and takes keys and values of such a page as zeros.
+ */
+typedef struct {
+  int B;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int table_width;                   /* pages per sequence; table_width * page_size < 2^31 */
+  const int32_t* seq_lens;           /* [B] */
+  const int32_t* cu_seqlens;         /* [B + 1] or NULL (not used by attention) */
+} sage_fp4_batch_t;
+
+/*
+ * Append keys and values: rows k, v [total, Hkv] (strides in elements of (head, token)) go to
+ * their pages, keys normed and rotated to their position on the way (rope, or NULL for
+ * neither); with q (heads > 0; x and y strided as sequence 0 of sage_fp4_rows_t) the same
+ * tokens' query heads are normed and rotated into y. Rows from cu_seqlens[B] on are left
+ * alone. A token whose position is beyond the rotation table is left out and reported like a
+ * bad page. Two tokens of one call must not share a slot. One launch.
+ */
+sage_status_t sage_fp4_cache_append(const sage_fp4_cache_t* cache, const sage_fp4_batch_t* batch,
+                                    const void* k, const int64_t k_stride[2], const void* v,
+                                    const int64_t v_stride[2], int total, const sage_fp4_rope_t* rope,
+                                    const sage_fp4_rows_t* q, void* stream);
+
+/* Read tokens back into dense rows k, v [total, Hkv] (strides of (head, token)); FP4 values are
+ * decoded exactly (every code times its scale fits both types). Rows without a token are left as
+ * they were. One launch. */
+sage_status_t sage_fp4_cache_gather(const sage_fp4_cache_t* cache, const sage_fp4_batch_t* batch, void* k,
+                                    const int64_t k_stride[2], void* v, const int64_t v_stride[2], int total,
+                                    void* stream);
+
+/* Workspace bytes of sage_fp4_attn_decode (host only; 0 for an empty or invalid problem). */
+size_t sage_fp4_decode_workspace_bytes(const sage_fp4_cache_t* cache, const sage_fp4_batch_t* batch, int Hq);
+
+/*
+ * Attention of one query per sequence over the cache: out[b, h] = softmax(sm_scale q[b, h] K^T) V
+ * over the seq_lens[b] tokens of sequence b and the key/value head h / (Hq / Hkv). q and out are
+ * [B, Hq, D] with strides of (sequence, head). A sequence of length 0 gets zeros. The batch's
+ * tokens are cut into equal shares, whatever the lengths, and the parts of a shared head
+ * joined by a second launch; results do not depend on timing. workspace: 256-byte aligned, at least
+ * sage_fp4_decode_workspace_bytes(); calls that may overlap need one each.
+ */
+sage_status_t sage_fp4_attn_decode(const sage_fp4_cache_t* cache, const sage_fp4_batch_t* batch, const void* q,
+                                   const int64_t q_stride[2], void* out, const int64_t o_stride[2], int Hq,
+                                   float sm_scale, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

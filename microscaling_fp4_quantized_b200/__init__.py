@@ -10,6 +10,7 @@ no CPU fallback: if the library cannot be loaded, every call raises.
     out = sage.attn(q, k, v, causal=False)          # q, k, v: [B, H, N, D] bf16/fp16 CUDA
     out = sage.sageattn(q, k, v, tensor_layout="NHD", is_causal=True)   # strided, GQA
     out = sage.sageattn_varlen(q, k, v, cu_q, cu_k, max_q, max_k)      # packed sequences
+    out = sage.sageattn_decode(q, cache, page_table, seq_lens)         # one token, paged cache
 """
 from __future__ import annotations
 
@@ -38,7 +39,8 @@ EXPORTED = [
     "sage_fp4_get_device_error", "sage_fp4_set_wait_timeout_ns", "sage_fp4_attn_fwd_noalloc",
     "sage_fp4_last_cuda_error", "sage_fp4_set_debug_flags", "sage_fp4_problem_sizes",
     "sage_fp4_quantize", "sage_fp4_attn_quantized", "sage_fp4_attn", "sage_fp4_mma_rate",
-    "sage_fp4_bounds_checked",
+    "sage_fp4_bounds_checked", "sage_fp4_norm_rope", "sage_fp4_cache_append", "sage_fp4_cache_gather",
+    "sage_fp4_decode_workspace_bytes", "sage_fp4_attn_decode",
 ]
 
 
@@ -122,9 +124,10 @@ def lib():
         L.sage_fp4_attn.argtypes = [pp, vp, vp, vp, vp, vp, sz, vp]
         L.sage_fp4_mma_rate.argtypes = [i, i, i, vp]
         L.sage_fp4_bounds_checked.argtypes = []
+        paged.bind(L)
         for n in EXPORTED[1:]:
             if n not in ("sage_fp4_quantize_scratch_bytes", "sage_fp4_workspace_bytes",
-                         "sage_fp4_last_cuda_error"):
+                         "sage_fp4_last_cuda_error", "sage_fp4_decode_workspace_bytes"):
                 getattr(L, n).restype = i  # sage_status_t
         _lib = L
     return _lib
@@ -272,12 +275,13 @@ def qk_scores(qz: dict, sm_scale: Optional[float] = None) -> torch.Tensor:
     return s
 
 
-DEV_ERR_TIMEOUT, DEV_ERR_SEQLENS, DEV_ERR_BOUNDS = 1, 2, 4
+DEV_ERR_TIMEOUT, DEV_ERR_SEQLENS, DEV_ERR_BOUNDS, DEV_ERR_PAGES = 1, 2, 4, 8
 
 
 def device_error(device=None) -> int:
     """Read and clear the device error word (synchronizes the current stream): bit 0 a
-    bounded wait ran out, bit 1 a packed problem's sequence table failed its check."""
+    bounded wait ran out, bit 1 a sequence table (or a length or position) failed its check,
+    bit 3 a page lay outside the cache."""
     w = ctypes.c_uint32(0)
     st = lib().sage_fp4_get_device_error(ctypes.byref(w), _stream(device))
     if st not in (SAGE_OK, SAGE_ERR_TIMEOUT, SAGE_ERR_INVALID_ARG, SAGE_ERR_BOUNDS):
@@ -558,3 +562,8 @@ class ProblemPlan:
     def attention(self, out: torch.Tensor) -> None:
         _check(lib().sage_fp4_attn_quantized(ctypes.byref(self.problem), ctypes.byref(self._qz), _ptr(out),
                                              _stream(self.device)), "sage_fp4_attn_quantized")
+
+
+from . import paged  # noqa: E402
+from .paged import (PagedKVCache, cache_append, cache_gather, decode_workspace_bytes,  # noqa: E402,F401
+                    qk_norm_rope, rope_table, sageattn_decode, sageattn_prefill)

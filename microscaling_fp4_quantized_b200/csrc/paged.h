@@ -1,0 +1,94 @@
+// Launch interfaces of the paged cache kernels (not part of the C ABI).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sage_internal.h"
+
+namespace sage {
+
+// n / d for 0 <= n < 2^31 by a multiply: with L = ceil(log2 d) and m = floor(2^(31+L) / d) + 1,
+// m d lies in (2^(31+L), 2^(31+L) + d], d <= 2^L, so n m / 2^(31+L) exceeds n / d by less than
+// n 2^L / (d 2^(31+L)) < 1 / d and has the same integer part.
+struct FastDiv {
+  uint32_t d, m, s;
+};
+
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t L = 0;
+  while ((uint64_t(1) << L) < d) ++L;
+  const unsigned __int128 m = ((unsigned __int128)1 << (31 + L)) / d + 1;
+  return FastDiv{d, static_cast<uint32_t>(m), 31 + L};
+}
+
+__device__ __forceinline__ uint32_t div_by_page(const FastDiv& f, uint32_t n) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(n) * f.m) >> f.s);
+}
+
+struct CacheView {
+  void *k, *v;
+  uint8_t *k_sf, *v_sf;
+  Strides sk, sv;  // elements of (page, head, slot)
+  int num_pages, Hkv;
+  FastDiv page;
+  const int32_t* table;
+  int64_t table_stride;
+  int capacity;  // table_width * page_size
+  const int32_t* lens;
+  const int32_t* cu;
+  int B;
+};
+
+// Norm, rotation, append: token rows of up to three sets of heads.
+struct RowsParams {
+  const void *q, *k, *v;
+  void *qo, *ko;         // dense outputs (ko unused when keys go to the cache)
+  Strides sq, sk, sv, sqo, sko;
+  int Hq, Hk, Hv;        // heads of each set (0: none)
+  int T, N;              // tokens in all; tokens per sequence (dense), T for packed ones
+  int heads_per_item, items_q, items_k, items_v;  // items along the heads
+  const void *qw, *kw;
+  int w32;
+  float eps;
+  const float* rope;
+  int rope_len, R, interleaved;
+  const int32_t* positions;
+  CacheView c;
+  uint32_t* err;
+};
+
+struct GatherParams {
+  void *k, *v;
+  Strides sk, sv;  // (unused, head, token)
+  int T, heads_per_item, items;
+  CacheView c;
+  uint32_t* err;
+};
+
+struct DecodeParams {
+  const void* q;
+  void* out;
+  int64_t sqb, sqh, sob, soh;
+  int Hq, group;       // query heads per key/value head
+  int chunks;          // chunks of the group, each with at most 8 * NT heads
+  int chunk_heads;     // query heads of a chunk (the last one may have fewer)
+  float scale_log2;    // sm_scale * log2(e)
+  CacheView c;
+  float* part_o;       // [grid, 2, 8 * NT, D]
+  float* part_ml;      // [grid, 2, 8 * NT, 2]
+  int4* rec;           // [joins] what is to be joined
+  int grid, joins;     // (set by launch_decode)
+  uint32_t* err;
+};
+
+constexpr int kTileKeys = 64;       // keys of a CTA tile of the decode kernel
+constexpr int kMaxDecodeCtas = 1184;  // 8 per SM: bound of the decode grid and of its workspace
+
+cudaError_t launch_rows(const RowsParams& p, int D, int dtype, bool to_cache, bool fp4, cudaStream_t stream);
+cudaError_t launch_gather(const GatherParams& p, int D, int dtype, bool fp4, cudaStream_t stream);
+// NT: 8-head column tiles per chunk (1 or 2). max_grid bounds the grid and the partials.
+cudaError_t launch_decode(const DecodeParams& p, int D, int dtype, bool fp4, int NT, int max_grid, cudaStream_t stream);
+
+}  // namespace sage

@@ -1,0 +1,454 @@
+// Row kernels of the paged cache (sm_100a): norm and rotation of query / key heads, the same
+// with keys and values going into cache pages, and reading pages back.
+//
+// One head of one token is a row of D channels. D / 16 lanes own a row, 16 channels each: the two
+// 8-channel chunks a lane owns are the two halves of 8 rotation pairs (i, i + R/2), so neither
+// pairing needs a shuffle; only the mean square and the FP4 block maximum cross lanes. A
+// lane group keeps its token's cosines, sines and norm weights in registers over the heads of
+// its item and has four rows' loads in flight. All three operations are bound by HBM: each row
+// is read once and written once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
+#include <cstdint>
+#include <type_traits>
+
+#include "fp4_encode.cuh"
+#include "paged.h"
+#include "sm100_ptx.cuh"
+
+namespace sage {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // rows in flight per lane group
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(uint4 raw, float* x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t r;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    r = *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(a, b);
+    r = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float* x) {
+  return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+}
+
+// Eight norm weights from channel c on.
+template <typename T>
+__device__ __forceinline__ void load_weights(const void* w, int w32, int c, float* x) {
+  if (w32) {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
+    const float4 a = __ldg(f), b = __ldg(f + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  } else {
+    unpack<T>(__ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(w) + c)), x);
+  }
+}
+
+// RN32(1 / sqrt(m)) of a binary64 m: the binary32 estimate refined by two Newton steps in
+// binary64 (each squares the relative error, ~2^-22 at first), so that the result is the
+// correctly rounded one up to the rare value within ~2^-50 of a rounding border. Outside
+// binary32's range, and for zero and NaN, the binary64 functions.
+__device__ __forceinline__ float rsqrt_exact(double m) {
+  if (!(m > 1e-36 && m < 1e37)) return static_cast<float>(1.0 / sqrt(m));
+  double y = static_cast<double>(rsqrtf(static_cast<float>(m)));
+  const double h = 0.5 * m;
+  y = y * fma(-h * y, y, 1.5);
+  y = y * fma(-h * y, y, 1.5);
+  return static_cast<float>(y);
+}
+
+// Where a token of an append or gather call lies in the cache.
+struct Place {
+  int64_t page;  // -1: nowhere (outside the sequences, or refused and reported)
+  int slot, pos;
+};
+
+__device__ __forceinline__ Place place_of(const CacheView& c, int tok, bool lead, uint32_t* err) {
+  Place r{-1, 0, 0};
+  int b = tok, first = tok, n = 1;
+  if (c.cu != nullptr) {
+    int lo = 0, hi = c.B;  // the last b with cu[b] <= tok
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(c.cu + mid) <= tok) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    first = __ldg(c.cu + b);
+    const int end = __ldg(c.cu + b + 1);
+    n = end - first;
+    if (tok < first || tok >= end) {  // rows behind the last sequence; before the first: a bad table
+      if (tok < first && lead) atomicOr(err, kDevErrSeqlens);
+      return r;
+    }
+  } else if (b >= c.B) {
+    return r;
+  }
+  const int len = __ldg(c.lens + b);
+  const int64_t pos = static_cast<int64_t>(len) - n + (tok - first);
+  if (pos < 0 || len > c.capacity) {
+    if (lead) atomicOr(err, kDevErrSeqlens);
+    return r;
+  }
+  r.pos = static_cast<int>(pos);
+  const uint32_t i = div_by_page(c.page, r.pos);
+  r.slot = r.pos - static_cast<int>(i * c.page.d);
+  const int page = __ldg(c.table + static_cast<int64_t>(b) * c.table_stride + i);
+  if (page < 0 || page >= c.num_pages) {
+    if (lead) atomicOr(err, kDevErrPages);
+    return r;
+  }
+  r.page = page;
+  return r;
+}
+
+}  // namespace
+
+// Item (token group, head range of one set): a warp holds 32 / (D / 16) tokens and walks the
+// heads. CACHE: keys and values go to their pages (FP4: quantized), else keys to dense rows.
+template <typename T, int D, bool CACHE, bool FP4>
+__global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RowsParams p) {
+  constexpr int LPR = D / 16, GPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, j = lane % LPR;
+  const int items = p.items_q + p.items_k + p.items_v;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  const int64_t tg = w / items;
+  int it = static_cast<int>(w - tg * items);
+  if (tg * GPW >= p.T) return;
+  const int64_t tok = tg * GPW + lane / LPR;
+  bool ok = tok < p.T;
+  // The item's set of heads.
+  int set = 0, H = p.Hq;
+  if (it >= p.items_q) {
+    it -= p.items_q;
+    set = 1;
+    H = p.Hk;
+    if (it >= p.items_k) {
+      it -= p.items_k;
+      set = 2;
+      H = p.Hv;
+    }
+  }
+  const int h0 = it * p.heads_per_item, h1 = min(H, h0 + p.heads_per_item);
+  const char* src = static_cast<const char*>(set == 0 ? p.q : set == 1 ? p.k : p.v);
+  const Strides ss = set == 0 ? p.sq : set == 1 ? p.sk : p.sv;
+
+  // The token's place and position.
+  Place at{-1, 0, 0};
+  int64_t b = 0, n = tok;
+  if (ok) {
+    if constexpr (CACHE) {
+      at = place_of(p.c, static_cast<int>(tok), j == 0, p.err);
+      ok = at.page >= 0;
+    } else {
+      b = tok / p.N;
+      n = tok - b * p.N;
+      at.pos = p.positions != nullptr ? __ldg(p.positions + tok) : static_cast<int>(n);
+    }
+    if (ok && p.rope != nullptr && (at.pos < 0 || at.pos >= p.rope_len)) {
+      if (j == 0) atomicOr(p.err, kDevErrSeqlens);
+      ok = false;
+    }
+  }
+  const int R = set == 2 || p.rope == nullptr ? 0 : p.R;
+  const int half = R / 16;
+  const bool rot = j < half;
+  const int ca = rot ? j : R / 8 + 2 * (j - half), cb = rot ? j + half : ca + 1;
+
+  float cs[8], sn[8];
+  if (ok && rot) {
+    const float* row = p.rope + static_cast<int64_t>(at.pos) * R;
+    const int oa = p.interleaved ? 4 * ca : 8 * ca, ob = p.interleaved ? 4 * cb : 8 * ca + 4;
+    const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + oa)), c1 = __ldg(reinterpret_cast<const float4*>(row + ob));
+    const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + R / 2 + oa)), s1 = __ldg(reinterpret_cast<const float4*>(row + R / 2 + ob));
+    cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w; cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
+    sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w; sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = 1.0f;
+      sn[i] = 0.0f;
+    }
+  }
+  const void* wp = set == 0 ? p.qw : set == 1 ? p.kw : nullptr;
+  float wt[16];
+  if (wp != nullptr) {
+    load_weights<T>(wp, p.w32, 8 * ca, wt);
+    load_weights<T>(wp, p.w32, 8 * cb, wt + 8);
+  }
+
+  const int64_t src_tok = b * ss.b + n * ss.n;
+  const bool paged = CACHE && set != 0;
+  const Strides ds = paged ? (set == 1 ? p.c.sk : p.c.sv) : (set == 0 ? p.sqo : p.sko);
+  const int64_t dst_tok = paged ? at.page * ds.b + at.slot * ds.n : b * ds.b + n * ds.n;
+  char* dst = static_cast<char*>(paged ? (set == 1 ? p.c.k : p.c.v) : set == 0 ? p.qo : p.ko);
+  uint8_t* sf = set == 1 ? p.c.k_sf : p.c.v_sf;
+
+  for (int h = h0; h < h1; h += kUnroll) {
+    uint4 raw[kUnroll][2];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+      if (ok && h + u < h1) {
+        const char* row = src + (src_tok + static_cast<int64_t>(h + u) * ss.h) * 2;
+        raw[u][0] = ld_stream(row + ca * 16);
+        raw[u][1] = ld_stream(row + cb * 16);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h + u >= h1) break;  // uniform over the warp
+      const int64_t row = dst_tok + static_cast<int64_t>(h + u) * ds.h;
+      if (!(FP4 && paged) && wp == nullptr && R == 0) {
+        if (ok) {
+          *reinterpret_cast<uint4*>(dst + row * 2 + ca * 16) = raw[u][0];
+          *reinterpret_cast<uint4*>(dst + row * 2 + cb * 16) = raw[u][1];
+        }
+        continue;
+      }
+      float x[16];
+      unpack<T>(raw[u][0], x);
+      unpack<T>(raw[u][1], x + 8);
+      if (wp != nullptr) {
+        // The mean square in binary64 (squares of 16-bit values are exact there): the norm then
+        // rounds the same way whatever the order of the sum, which 4-bit codes depend on.
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), s);
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        double ms = s * (1.0 / D) + static_cast<double>(p.eps);
+        if (ms < 1e-70 && ms > 0.0) {  // rows of subnormals: their inverse would leave binary32
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] *= 18446744073709551616.0f;  // 2^64, exact
+          ms *= 340282366920938463463374607431768211456.0;               // 2^128
+        }
+        const float r = rsqrt_exact(ms);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), wt[i]);
+      }
+      if (rot) {
+        // Products and sums each rounded on their own (no fused multiply-add), as a chain of
+        // elementwise operations rounds them: codes then agree bit for bit.
+        if (p.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float a = x[2 * i], c = x[2 * i + 1];
+            x[2 * i] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(c, sn[i]));
+            x[2 * i + 1] = __fadd_rn(__fmul_rn(c, cs[i]), __fmul_rn(a, sn[i]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float a = x[i], c = x[i + 8];
+            x[i] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(c, sn[i]));
+            x[i + 8] = __fadd_rn(__fmul_rn(c, cs[i]), __fmul_rn(a, sn[i]));
+          }
+        }
+      }
+      if (FP4 && paged) {
+        float ma = 0.0f, mb = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          x[i] = fmaxf(fminf(x[i], FLT_MAX), -FLT_MAX);  // saturate (NaN: to the largest)
+          if (i < 8) ma = fmaxf(ma, fabsf(x[i]));
+          else mb = fmaxf(mb, fabsf(x[i]));
+        }
+        // A block is two neighbouring chunks: this lane's two, or one each of lanes j and j ^ 1.
+        const float na = __shfl_xor_sync(0xffffffffu, ma, 1), nb = __shfl_xor_sync(0xffffffffu, mb, 1);
+        const uint32_t ba = block_scale_byte(fmaxf(ma, rot ? na : mb)), bb = block_scale_byte(fmaxf(mb, rot ? nb : ma));
+        const uint32_t wa = encode8_neg<0>(x, e4m3_to_f32(ba)), wb = encode8_neg<8>(x, e4m3_to_f32(bb));
+        if (ok) {
+          char* codes = dst + row / 2;
+          uint8_t* scales = sf + row / 16;
+          if (rot) {
+            *reinterpret_cast<uint32_t*>(codes + 4 * ca) = wa;
+            *reinterpret_cast<uint32_t*>(codes + 4 * cb) = wb;
+            if ((j & 1) == 0) {
+              scales[ca / 2] = static_cast<uint8_t>(ba);
+              scales[cb / 2] = static_cast<uint8_t>(bb);
+            }
+          } else {
+            *reinterpret_cast<uint2*>(codes + 4 * ca) = make_uint2(wa, wb);
+            scales[ca / 2] = static_cast<uint8_t>(ba);
+          }
+        }
+      } else if (ok) {
+        *reinterpret_cast<uint4*>(dst + row * 2 + ca * 16) = pack<T>(x);
+        *reinterpret_cast<uint4*>(dst + row * 2 + cb * 16) = pack<T>(x + 8);
+      }
+    }
+  }
+}
+
+// Item (token group, head range of K or of V): rows of the cache to dense rows.
+template <typename T, int D, bool FP4>
+__global__ void __launch_bounds__(kThreads, 2) gather_kernel(const GatherParams p) {
+  constexpr int LPR = D / 16, GPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, j = lane % LPR;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  const int64_t tg = w / (2 * p.items);
+  int it = static_cast<int>(w - tg * (2 * p.items));
+  if (tg * GPW >= p.T) return;
+  const int64_t tok = tg * GPW + lane / LPR;
+  if (tok >= p.T) return;  // no shuffles below
+  const bool is_v = it >= p.items;
+  if (is_v) it -= p.items;
+  const int h0 = it * p.heads_per_item, h1 = min(p.c.Hkv, h0 + p.heads_per_item);
+  const Place at = place_of(p.c, static_cast<int>(tok), j == 0, p.err);
+  if (at.page < 0) return;
+  const Strides ss = is_v ? p.c.sv : p.c.sk, ds = is_v ? p.sv : p.sk;
+  const char* src = static_cast<const char*>(is_v ? p.c.v : p.c.k);
+  const uint8_t* sf = is_v ? p.c.v_sf : p.c.k_sf;
+  char* dst = static_cast<char*>(is_v ? p.v : p.k) + (tok * ds.n + 16 * j) * 2;
+  const int64_t src_tok = at.page * ss.b + at.slot * ss.n;
+  for (int h = h0; h < h1; h += kUnroll) {
+    uint4 raw[kUnroll][2];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h + u >= h1) continue;
+      const int64_t row = src_tok + static_cast<int64_t>(h + u) * ss.h;
+      if constexpr (FP4) {
+        const uint2 codes = *reinterpret_cast<const uint2*>(src + row / 2 + 8 * j);
+        raw[u][0] = make_uint4(codes.x, codes.y, sf[row / 16 + j], 0);
+      } else {
+        raw[u][0] = ld_stream(src + row * 2 + j * 32);
+        raw[u][1] = ld_stream(src + row * 2 + j * 32 + 16);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h + u >= h1) continue;
+      if constexpr (FP4) {
+        // E2M1 times E4M3 has at most six significant bits and fits fp16's range: every product
+        // below is exact, in fp16 and after it in bf16.
+        const float sc = e4m3_to_f32(raw[u][0].z);
+        const __half2 s2 = __floats2half2_rn(sc, sc);
+        uint32_t o[8];
+        const uint32_t wd[2] = {raw[u][0].x, raw[u][0].y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t v[4];
+          e2m1x8_to_f16x2(wd[i], v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&v[e]), s2);
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+              const float2 f = __half22float2(m);
+              o[4 * i + e] = pack2<T>(f.x, f.y);
+            } else {
+              o[4 * i + e] = *reinterpret_cast<const uint32_t*>(&m);
+            }
+          }
+        }
+        raw[u][0] = make_uint4(o[0], o[1], o[2], o[3]);
+        raw[u][1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      char* row = dst + static_cast<int64_t>(h + u) * ds.h * 2;
+      *reinterpret_cast<uint4*>(row) = raw[u][0];
+      *reinterpret_cast<uint4*>(row + 16) = raw[u][1];
+    }
+  }
+}
+
+template <typename T, int D>
+static cudaError_t rows_of(const RowsParams& p, bool to_cache, bool fp4, unsigned grid, cudaStream_t stream) {
+  if (!to_cache) rows_kernel<T, D, false, false><<<grid, kThreads, 0, stream>>>(p);
+  else if (fp4) rows_kernel<T, D, true, true><<<grid, kThreads, 0, stream>>>(p);
+  else rows_kernel<T, D, true, false><<<grid, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// Heads a warp walks: as many as leave enough warps to fill the machine (148 SMs, two
+// blocks of eight warps each), at most 16.
+static int heads_of(int64_t groups, int heads) {
+  int n = 16;
+  while (n > 1 && groups * ((heads + n - 1) / n) < 2 * 148 * 16) n /= 2;
+  return n;
+}
+
+cudaError_t launch_rows(const RowsParams& in, int D, int dtype, bool to_cache, bool fp4, cudaStream_t stream) {
+  RowsParams p = in;
+  const int gpw = 512 / D;
+  const int64_t groups = (static_cast<int64_t>(p.T) + gpw - 1) / gpw;
+  p.heads_per_item = heads_of(groups, p.Hq + p.Hk + p.Hv);
+  auto items = [&](int h) { return (h + p.heads_per_item - 1) / p.heads_per_item; };
+  p.items_q = items(p.Hq);
+  p.items_k = items(p.Hk);
+  p.items_v = items(p.Hv);
+  const int64_t warps = groups * (p.items_q + p.items_k + p.items_v);
+  const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (dtype == kDtypeBF16)
+    return D == 128 ? rows_of<__nv_bfloat16, 128>(p, to_cache, fp4, grid, stream)
+                    : rows_of<__nv_bfloat16, 64>(p, to_cache, fp4, grid, stream);
+  return D == 128 ? rows_of<__half, 128>(p, to_cache, fp4, grid, stream)
+                  : rows_of<__half, 64>(p, to_cache, fp4, grid, stream);
+}
+
+template <typename T, int D>
+static void gather_of(const GatherParams& p, bool fp4, unsigned grid, cudaStream_t stream) {
+  if (fp4) gather_kernel<T, D, true><<<grid, kThreads, 0, stream>>>(p);
+  else gather_kernel<T, D, false><<<grid, kThreads, 0, stream>>>(p);
+}
+
+cudaError_t launch_gather(const GatherParams& in, int D, int dtype, bool fp4, cudaStream_t stream) {
+  GatherParams p = in;
+  const int gpw = 512 / D;
+  const int64_t groups = (static_cast<int64_t>(p.T) + gpw - 1) / gpw;
+  p.heads_per_item = heads_of(groups, 2 * p.c.Hkv);
+  p.items = (p.c.Hkv + p.heads_per_item - 1) / p.heads_per_item;
+  const int64_t warps = groups * 2 * p.items;
+  const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (dtype == kDtypeBF16) {
+    if (D == 128) gather_of<__nv_bfloat16, 128>(p, fp4, grid, stream);
+    else gather_of<__nv_bfloat16, 64>(p, fp4, grid, stream);
+  } else {
+    if (D == 128) gather_of<__half, 128>(p, fp4, grid, stream);
+    else gather_of<__half, 64>(p, fp4, grid, stream);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace sage

@@ -457,6 +457,11 @@ sage_fp4_problem_t dense_problem(int B, int H, int N, int D, int dtype, int caus
 
 }  // namespace
 
+namespace sage {
+int device_error_word(uint32_t** out) { return error_word(out); }
+int status_of(cudaError_t e) { return cuda_status(e); }
+}  // namespace sage
+
 extern "C" {
 
 const char* sage_status_string(sage_status_t status) {

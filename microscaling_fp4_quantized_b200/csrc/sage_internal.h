@@ -11,7 +11,7 @@ namespace sage {
 enum : int { kDtypeBF16 = 0, kDtypeF16 = 1 };
 
 // Bits of the device error word.
-enum : uint32_t { kDevErrTimeout = 1u, kDevErrSeqlens = 2u, kDevErrBounds = 4u };
+enum : uint32_t { kDevErrTimeout = 1u, kDevErrSeqlens = 2u, kDevErrBounds = 4u, kDevErrPages = 8u };
 
 // Extents the kernels may touch, derived on the host from the problem: elements of the
 // caller's q, k, v and out reachable through the strides, bytes of each quantized
@@ -212,5 +212,11 @@ cudaError_t launch_attention8(const TensorMaps& maps, const AttnParams& p, int t
 // Tensor-core rate probe (mma_rate.cu): `ctas` CTAs, each issuing `iters` block-scaled FP4
 // products of M = 128, N = n, K = 64.
 cudaError_t launch_mma_rate(int n, int iters, int ctas, uint32_t* err, uint64_t timeout_ns, cudaStream_t stream);
+
+// Host services of sage_api.cu for the other entry points: the device error word's address
+// on the current device, and the status (with its text kept) of a CUDA error. Both return
+// a sage_status_t.
+int device_error_word(uint32_t** out);
+int status_of(cudaError_t e);
 
 }  // namespace sage

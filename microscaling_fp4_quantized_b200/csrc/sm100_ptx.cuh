@@ -335,6 +335,18 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1(float a0, float a1, float b0, 
   return w;
 }
 
+// Eight E2M1 codes (low nibble first) -> four words of two fp16 values each.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&v)[4]) {
+  asm("{\n\t.reg .b8 x0, x1, x2, x3;\n\t"
+      "mov.b32 {x0, x1, x2, x3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, x0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, x1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, x2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, x3;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+}
+
 // Packed two-lane FP32 arithmetic (one instruction for two values).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;

@@ -1,0 +1,405 @@
+"""Paged key/value cache: norm and rotation of heads, append, dense read, one-token attention.
+
+The entry points wrap the calls of the same names in ``include/sage_fp4.h``. As in the rest of the package
+they check arguments, allocate outputs and workspace with torch and launch on the current
+stream of the tensors' device; what the device tables hold (lengths, pages, positions) is checked on
+the device and reported by ``device_error()``.
+
+    cache = sage.PagedKVCache.empty(num_pages, 64, num_kv_heads, head_dim, format="fp4")
+    rope = sage.rope_table(max_positions, head_dim)
+    # prompts: packed rows, seq_lens = their lengths
+    out = sage.sageattn_prefill(q, k, v, cache, page_table, seq_lens, cu_seqlens, max_seqlen, rope=rope)
+    # one token of each sequence: seq_lens += 1, then
+    q = sage.cache_append(cache, k, v, page_table, seq_lens, q=q, rope=rope)
+    out = sage.sageattn_decode(q, cache, page_table, seq_lens)
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+import microscaling_fp4_quantized_b200 as _sage
+
+CACHE_FORMAT = {"16bit": 0, "fp4": 1}
+_NULL = contextlib.nullcontext()
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_f32", ctypes.c_int),
+                ("eps", ctypes.c_float), ("rope", ctypes.c_void_p), ("rope_len", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_sf", ctypes.c_void_p),
+                ("v_sf", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_width", ctypes.c_int), ("seq_lens", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p)]
+
+
+_Stride2 = ctypes.c_int64 * 2
+_Stride3 = ctypes.c_int64 * 3
+
+
+def bind(L) -> None:
+    """Argument types of the paged entry points."""
+    i, vp, sz, f = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+    rows, rope, cache, batch = (ctypes.POINTER(t) for t in (_Rows, _Rope, _Cache, _Batch))
+    st = ctypes.POINTER(ctypes.c_int64)
+    L.sage_fp4_norm_rope.argtypes = [rows, rows, i, i, i, i, rope, vp, vp]
+    L.sage_fp4_cache_append.argtypes = [cache, batch, vp, st, vp, st, i, rope, rows, vp]
+    L.sage_fp4_cache_gather.argtypes = [cache, batch, vp, st, vp, st, i, vp]
+    L.sage_fp4_decode_workspace_bytes.argtypes = [cache, batch, i]
+    L.sage_fp4_decode_workspace_bytes.restype = sz
+    L.sage_fp4_attn_decode.argtypes = [cache, batch, vp, st, vp, st, i, f, vp, sz, vp]
+
+
+def _on(device: torch.device):
+    """Makes `device` the current one for a launch."""
+    return _NULL if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _stride(t: torch.Tensor, d: int) -> int:
+    """A dimension of size 1 has no stride that could matter."""
+    return t.stride(d) if t.shape[d] != 1 else 0
+
+
+def _check_rows(name: str, t: torch.Tensor, dim: int, dtype: torch.dtype, device: torch.device) -> None:
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if t.shape[-1] != 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the channel (last) dimension must be contiguous")
+
+
+def _check_table(name: str, t: torch.Tensor, shape: tuple, device: torch.device) -> None:
+    if not t.is_cuda or t.device != device or t.dtype != torch.int32:
+        raise ValueError(f"{name} must be an int32 CUDA tensor on {device}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {list(shape)}")
+
+
+def _rope(D: int, dtype: torch.dtype, device: torch.device, q_weight, k_weight, eps: float, rope,
+          interleaved: bool) -> Optional[_Rope]:
+    if q_weight is None and k_weight is None and rope is None:
+        return None
+    r = _Rope()
+    wdt = None
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if not w.is_cuda or w.device != device or tuple(w.shape) != (D,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{D}] CUDA tensor on {device}")
+        if w.dtype not in (dtype, torch.float32) or wdt not in (None, w.dtype):
+            raise ValueError(f"norm weights must both be {dtype} or both float32")
+        wdt = w.dtype
+        setattr(r, name, w.data_ptr())
+    r.weight_f32 = int(wdt == torch.float32)
+    r.eps = float(eps)
+    if rope is not None:
+        if not rope.is_cuda or rope.device != device or rope.dtype != torch.float32 or rope.dim() != 2:
+            raise ValueError(f"rope must be a float32 CUDA tensor [positions, rotary_dim] on {device}")
+        if not rope.is_contiguous():
+            raise ValueError("rope must be contiguous")
+        # A table of no positions has no address; any non-null one says that there is a table.
+        r.rope = rope.data_ptr() or 16
+        r.rope_len, r.rotary_dim = rope.shape
+    r.interleaved = int(bool(interleaved))
+    return r
+
+
+def _rows(x: torch.Tensor, y: torch.Tensor, heads: int, dims: tuple) -> _Rows:
+    sx = _Stride3(*(_stride(x, d) if d >= 0 else 0 for d in dims))
+    sy = _Stride3(*(_stride(y, d) if d >= 0 else 0 for d in dims))
+    return _Rows(x.data_ptr(), y.data_ptr(), heads, sx, sy)
+
+
+def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The rotation table the entry points take, [max_positions, rotary_dim] float32: the cosines of
+    position * base^(-2i / rotary_dim), i < rotary_dim / 2, then their sines. The angles are formed
+    in 64 bits (at far positions 32 would lose the turn). Built once per model."""
+    if max_positions < 0 or rotary_dim <= 0 or rotary_dim % 32 != 0:
+        raise ValueError("rotary_dim must be a positive multiple of 32 and max_positions not negative")
+    inv = float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
+    a = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat((a.cos(), a.sin()), dim=1).float()
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, rope: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, interleaved: bool = False, tensor_layout: str = "HND",
+                 q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """RMS norm of every query and key head and the position rotation, in one pass over q and k.
+
+    q and k: [B, H, N, D] ("HND"), [B, N, H, D] ("NHD") or packed [tokens, H, D], bf16 or fp16, any strides
+    with contiguous channels; k may have fewer heads and may be left out. Weights ([D], the tensors' dtype
+    or float32) switch the norm on; rope (see rope_table) the rotation of the first rope.shape[1] channels,
+    pairs (i, i + rotary_dim/2), or (2i, 2i+1) when interleaved. positions: int32, [B, N] or, for packed
+    rows, [tokens]; without it token n of a 4-d tensor is at position n. A position outside the table
+    is reported by device_error() and its rows are not written. q_out / k_out may be q / k (in place) and
+    must not overlap them otherwise. Returns (q_out, k_out)."""
+    if q.dim() == 3:
+        dims, shape = (-1, 1, 0), (q.shape[0],)
+        if rope is not None and positions is None:
+            raise ValueError("packed rows need positions")
+    elif q.dim() == 4 and tensor_layout in ("HND", "NHD"):
+        dims = (0, 1, 2) if tensor_layout == "HND" else (0, 2, 1)
+        shape = (q.shape[0], q.shape[dims[2]])
+    else:
+        raise ValueError("q must be [B, H, N, D] ('HND'), [B, N, H, D] ('NHD') or [tokens, H, D]")
+    D, dev, dtype = q.shape[-1], q.device, q.dtype
+    code = _sage._dtype_code(dtype)
+    _check_rows("q", q, q.dim(), dtype, dev)
+    if k is not None:
+        _check_rows("k", k, q.dim(), dtype, dev)
+        if k.shape[-1] != D or tuple(k.shape[d] for d in (dims[0], dims[2]) if d >= 0) != shape:
+            raise ValueError("q and k disagree on batch, tokens or head dimension")
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    if positions is not None:
+        _check_table("positions", positions, shape, dev)
+    r = _rope(D, dtype, dev, q_weight, k_weight, eps, rope, interleaved)
+    outs = []
+    for name, x, y in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if x is not None and y is not None:
+            _check_rows(name, y, q.dim(), dtype, dev)
+            if y.shape != x.shape:
+                raise ValueError(f"{name} must have the shape of its input")
+        outs.append(torch.empty(x.shape, dtype=dtype, device=dev) if x is not None and y is None else y)
+    q_out, k_out = outs
+    B, N = (1,) + shape if len(shape) == 1 else shape
+    qr = _rows(q, q_out, q.shape[dims[1]], dims)
+    kr = _rows(k, k_out, k.shape[dims[1]], dims) if k is not None else None
+    with _on(dev):
+        _sage._check(_sage.lib().sage_fp4_norm_rope(qr, kr, B, N, D, code, r, _sage._ptr(positions), _sage._stream(dev)),
+                     "sage_fp4_norm_rope")
+    return q_out, k_out
+
+
+class PagedKVCache:
+    """The pages of one layer's keys and values, on the caller's buffers.
+
+    k, v: [pages, heads, slots, D] ("HND") or [pages, slots, heads, D] ("NHD"), any strides with contiguous
+    channels. 16-bit: bf16 or fp16. FP4: uint8 codes with D / 2 bytes per row, and k_sf, v_sf uint8 with D / 16
+    bytes per row and an eighth of the codes' strides; `dtype` then names the dense side (queries, new
+    keys and values, outputs)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_sf: Optional[torch.Tensor] = None,
+                 v_sf: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                 tensor_layout: str = "HND"):
+        if tensor_layout not in ("HND", "NHD"):
+            raise ValueError("tensor_layout must be 'HND' or 'NHD'")
+        fp4 = k.dtype == torch.uint8
+        if fp4 and (k_sf is None or v_sf is None or dtype is None):
+            raise ValueError("an FP4 cache needs k_sf, v_sf and dtype")
+        if not fp4 and (k_sf is not None or v_sf is not None or dtype not in (None, k.dtype)):
+            raise ValueError("a 16-bit cache has no scales, and its own dtype")
+        for name, t in (("k", k), ("v", v)) + ((("k_sf", k_sf), ("v_sf", v_sf)) if fp4 else ()):
+            _check_rows(name, t, 4, k.dtype, k.device)
+        if k.shape != v.shape:
+            raise ValueError("k and v must have the same shape")
+        dims = (0, 1, 2) if tensor_layout == "HND" else (0, 2, 1)
+        D = k.shape[3] * (2 if fp4 else 1)
+        if fp4:
+            for c, s in ((k, k_sf), (v, v_sf)):
+                if tuple(s.shape) != tuple(k.shape[:3]) + (D // 16,):
+                    raise ValueError("scales must have the codes' shape with D / 16 bytes per row")
+                if any(c.shape[d] > 1 and c.stride(d) != 8 * s.stride(d) for d in range(3)):
+                    raise ValueError("scales must have an eighth of the codes' strides")
+        self.k, self.v, self.k_sf, self.v_sf = k, v, k_sf, v_sf
+        self.format = "fp4" if fp4 else "16bit"
+        self.dtype = dtype if fp4 else k.dtype
+        self.tensor_layout = tensor_layout
+        self.device = k.device
+        self.num_pages, self.num_kv_heads, self.page_size = (k.shape[d] for d in dims)
+        self.head_dim = D
+        unit = 2 if fp4 else 1  # elements per code byte
+        ks, vs = (_Stride3(*(unit * _stride(t, d) for d in dims)) for t in (k, v))
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), k_sf.data_ptr() if fp4 else None, v_sf.data_ptr() if fp4 else None,
+                         ks, vs, self.num_pages, self.page_size, self.num_kv_heads, D, _sage._dtype_code(self.dtype),
+                         CACHE_FORMAT[self.format])
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
+              format: str = "16bit", tensor_layout: str = "HND", device="cuda") -> "PagedKVCache":
+        """A cache on buffers of its own (not initialised: only appended tokens are ever read)."""
+        if format not in CACHE_FORMAT:
+            raise ValueError(f"format must be one of {tuple(CACHE_FORMAT)}")
+        rows = (num_pages, num_kv_heads, page_size) if tensor_layout == "HND" else (num_pages, page_size, num_kv_heads)
+        if format == "16bit":
+            k, v = (torch.empty(rows + (head_dim,), dtype=dtype, device=device) for _ in range(2))
+            return cls(k, v, tensor_layout=tensor_layout)
+        k, v = (torch.empty(rows + (head_dim // 2,), dtype=torch.uint8, device=device) for _ in range(2))
+        ks, vs = (torch.empty(rows + (head_dim // 16,), dtype=torch.uint8, device=device) for _ in range(2))
+        return cls(k, v, ks, vs, dtype=dtype, tensor_layout=tensor_layout)
+
+    def _batch(self, page_table: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor]) -> _Batch:
+        dev = self.device
+        if not page_table.is_cuda or page_table.device != dev or page_table.dtype != torch.int32:
+            raise ValueError(f"page_table must be an int32 CUDA tensor on {dev}")
+        if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table must be [sequences, pages] with contiguous rows")
+        B, width = page_table.shape
+        _check_table("seq_lens", seq_lens, (B,), dev)
+        if cu_seqlens is not None:
+            _check_table("cu_seqlens", cu_seqlens, (B + 1,), dev)
+        return _Batch(B, page_table.data_ptr(), _stride(page_table, 0), width, seq_lens.data_ptr(),
+                      cu_seqlens.data_ptr() if cu_seqlens is not None else None)
+
+    def _dense(self, name: str, t: torch.Tensor, total: Optional[int]) -> None:
+        _check_rows(name, t, 3, self.dtype, self.device)
+        if tuple(t.shape[1:]) != (self.num_kv_heads, self.head_dim) or total not in (None, t.shape[0]):
+            raise ValueError(f"{name} must be [tokens, {self.num_kv_heads}, {self.head_dim}]")
+
+
+def cache_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
+                 seq_lens: torch.Tensor, *, cu_seqlens: Optional[torch.Tensor] = None,
+                 q: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, rope: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Append keys and values [tokens, Hkv, D] to their sequences' pages, the keys normed and rotated to their
+    positions on the way (see qk_norm_rope); FP4 caches quantize them.
+
+    page_table int32 [B, pages], seq_lens int32 [B]: lengths with the new tokens. Rows cu_seqlens[b] ..
+    cu_seqlens[b+1] are the last tokens of sequence b (int32 [B+1]; without it one row per sequence); rows
+    behind cu_seqlens[B] are left alone. With q [tokens, Hq, D] the same tokens' queries are normed and rotated
+    too, into q_out (may be q), which is returned. Two tokens of a call must not share a slot. A page
+    outside the cache, a negative position and one beyond the rotation table are reported by
+    device_error(); such a token is left out."""
+    batch = cache._batch(page_table, seq_lens, cu_seqlens)
+    cache._dense("k", k, None)
+    total, dev, D = k.shape[0], cache.device, cache.head_dim
+    cache._dense("v", v, total)
+    if cu_seqlens is None and total != batch.B:
+        raise ValueError("without cu_seqlens, k and v hold one token per sequence")
+    r = _rope(D, cache.dtype, dev, q_weight, k_weight, eps, rope, interleaved)
+    rows = None
+    if q is not None:
+        _check_rows("q", q, 3, cache.dtype, dev)
+        if q.shape[0] != total or q.shape[2] != D:
+            raise ValueError(f"q must be [{total}, heads, {D}]")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _check_rows("q_out", q_out, 3, cache.dtype, dev)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have the shape of q")
+        rows = _rows(q, q_out, q.shape[1], (-1, 1, 0))
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    ks, vs = (_Stride2(_stride(t, 1), _stride(t, 0)) for t in (k, v))
+    with _on(dev):
+        _sage._check(_sage.lib().sage_fp4_cache_append(cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs, total, r, rows,
+                                                       _sage._stream(dev)), "sage_fp4_cache_append")
+    return q_out
+
+
+def cache_gather(cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, *,
+                 cu_seqlens: Optional[torch.Tensor] = None, total: Optional[int] = None,
+                 k_out: Optional[torch.Tensor] = None,
+                 v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Keys and values of the last cu_seqlens[b+1] - cu_seqlens[b] tokens of each sequence as packed rows
+    [total, Hkv, D] (without cu_seqlens: of the last one). total counts the rows; it is needed with
+    cu_seqlens unless k_out and v_out are given, and may be larger than cu_seqlens[B]. Rows without a
+    token are not written. FP4 values are decoded exactly. Returns (k_out, v_out)."""
+    batch = cache._batch(page_table, seq_lens, cu_seqlens)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("pass both of k_out and v_out, or neither")
+    if total is None:
+        if k_out is None and cu_seqlens is not None:
+            raise ValueError("cu_seqlens needs total, the number of rows")
+        total = k_out.shape[0] if k_out is not None else batch.B
+    if total < 0 or (cu_seqlens is None and total != batch.B):
+        raise ValueError("without cu_seqlens there is one row per sequence")
+    if k_out is None:
+        shape = (total, cache.num_kv_heads, cache.head_dim)
+        k_out, v_out = (torch.empty(shape, dtype=cache.dtype, device=cache.device) for _ in range(2))
+    else:
+        cache._dense("k_out", k_out, total)
+        cache._dense("v_out", v_out, total)
+    ks, vs = (_Stride2(_stride(t, 1), _stride(t, 0)) for t in (k_out, v_out))
+    with _on(cache.device):
+        _sage._check(_sage.lib().sage_fp4_cache_gather(cache._c, batch, k_out.data_ptr(), ks, v_out.data_ptr(), vs, total,
+                                                       _sage._stream(cache.device)), "sage_fp4_cache_gather")
+    return k_out, v_out
+
+
+def decode_workspace_bytes(cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, num_q_heads: int) -> int:
+    """Workspace of sageattn_decode for these shapes."""
+    batch = cache._batch(page_table, seq_lens, None)
+    return int(_sage.lib().sage_fp4_decode_workspace_bytes(cache._c, batch, num_q_heads))
+
+
+def sageattn_decode(q: torch.Tensor, cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, *,
+                    sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of one new token per sequence, q [B, Hq, D], over the seq_lens[b] cached tokens of its sequence
+    (its own key and value among them, once appended). Hq is a multiple of the cache's heads. A sequence
+    of length 0 gets zeros; a length outside the page table is clamped and a page outside the cache counts
+    as zeros, both reported by device_error(). workspace: uint8, 256-byte aligned, of at least
+    decode_workspace_bytes(); one that calls share must not serve two at once (allocated per call
+    when left out)."""
+    batch = cache._batch(page_table, seq_lens, None)
+    dev, Hq = cache.device, q.shape[1] if q.dim() == 3 else 0
+    for name, t in (("q", q),) if out is None else (("q", q), ("out", out)):
+        _check_rows(name, t, 3, cache.dtype, dev)
+        if tuple(t.shape) != (batch.B, Hq, cache.head_dim):
+            raise ValueError(f"{name} must be [{batch.B}, heads, {cache.head_dim}]")
+    if Hq % cache.num_kv_heads != 0:
+        raise ValueError("the number of query heads must be a multiple of the cache's heads")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    L = _sage.lib()
+    need = L.sage_fp4_decode_workspace_bytes(cache._c, batch, Hq)
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    elif not workspace.is_cuda or workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 CUDA tensor on {dev}")
+    qs, os_ = (_Stride2(_stride(t, 0), _stride(t, 1)) for t in (q, out))
+    with _on(dev):
+        _sage._check(L.sage_fp4_attn_decode(cache._c, batch, q.data_ptr(), qs, out.data_ptr(), os_, Hq, float(sm_scale or 0.0),
+                                            workspace.data_ptr(), workspace.numel(), _sage._stream(dev)),
+                     "sage_fp4_attn_decode")
+    return out
+
+
+def sageattn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, page_table: torch.Tensor,
+                     seq_lens: torch.Tensor, cu_seqlens: torch.Tensor, max_seqlen: int, *,
+                     cu_seqlens_kv: Optional[torch.Tensor] = None, max_seqlen_kv: Optional[int] = None,
+                     total_kv: Optional[int] = None, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, rope: Optional[torch.Tensor] = None,
+                     interleaved: bool = False, is_causal: bool = True, **attn) -> torch.Tensor:
+    """Prompts into the cache and their attention: cache_append (with q), cache_gather, sageattn_varlen.
+
+    q [tokens, Hq, D], k, v [tokens, Hkv, D] packed by cu_seqlens; seq_lens as in cache_append. Prompts that
+    continue a cached prefix attend to all of it: cu_seqlens_kv (offsets of the whole sequences, the sums of
+    seq_lens), max_seqlen_kv and total_kv then describe the keys. Keys and values are read back from the
+    cache, so the prompt sees what later tokens will see, an FP4 cache's rounding included. Further keyword
+    arguments go to sageattn_varlen."""
+    if (cu_seqlens_kv is None) != (max_seqlen_kv is None) or (cu_seqlens_kv is None) != (total_kv is None):
+        raise ValueError("cu_seqlens_kv, max_seqlen_kv and total_kv go together")
+    if cu_seqlens_kv is None:
+        cu_seqlens_kv, max_seqlen_kv, total_kv = cu_seqlens, max_seqlen, k.shape[0]
+    q = cache_append(cache, k, v, page_table, seq_lens, cu_seqlens=cu_seqlens, q=q, q_weight=q_weight, k_weight=k_weight,
+                     eps=eps, rope=rope, interleaved=interleaved)
+    k, v = cache_gather(cache, page_table, seq_lens, cu_seqlens=cu_seqlens_kv, total=total_kv)
+    with _on(cache.device):
+        return _sage.sageattn_varlen(q, k, v, cu_seqlens, cu_seqlens_kv, max_seqlen, max_seqlen_kv, is_causal=is_causal,
+                                     **attn)
