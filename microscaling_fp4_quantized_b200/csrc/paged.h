@@ -48,7 +48,8 @@ struct RowsParams {
   Strides sq, sk, sv, sqo, sko;
   int Hq, Hk, Hv;        // heads of each set (0: none)
   int T, N;              // tokens in all; tokens per sequence (dense), T for packed ones
-  int heads_per_item, items_q, items_k, items_v;  // items along the heads
+  int items_q, items_k, items_v;  // items along the heads of each set (set by launch_rows)
+  int per_q, per_k, per_v;        // heads of an item
   const void *qw, *kw;
   int w32;
   float eps;

@@ -366,6 +366,15 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2,%3};\n\tmov.b64 q, {%4,%5};\n\t"
+      "sub.rn.f32x2 s, p, q;\n\tmov.b64 {%0,%1}, s;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2,%3};\n\tmov.b64 q, {%4,%5};\n\t"

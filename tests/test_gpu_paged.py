@@ -1,7 +1,9 @@
 """Paged cache operators on the GPU against plain 64-bit implementations.
 
 Tolerances. u = eps / 2 of the output type (one rounding: half a step, relative). Norm and rotation run in
-binary32 with at most six roundings of 2^-24 on the way to each of the two products of a rotated channel;
+binary32: the mean square is a sum of at most 4 fused steps per accumulator, 3 additions in the lane and 3 over
+lanes, its scaling and eps (12 roundings of 2^-24, halved by the root), the reciprocal root is good to 2 units
+in the last place (4 x 2^-24), then two products, the rotation's product and its sum: 14, bounded by 16;
 attention adds its own terms (decode_tolerance). FP4 codes and scales, copies and reads are exact.
 """
 import numpy as np
@@ -57,7 +59,7 @@ def rows64(x, w, rope, pos, interleaved):
         m[..., a] = mag[..., a] * c.abs() + mag[..., b] * s.abs()
         m[..., b] = mag[..., b] * c.abs() + mag[..., a] * s.abs()
         z, mag = y, m
-    return z, 6 * 2.0 ** -24 * mag
+    return z, 16 * 2.0 ** -24 * mag
 
 
 def assert_rounded(got, want, slack, dtype):
@@ -328,7 +330,8 @@ def test_append_and_gather(sage, oracle_mod, fmt, dtype, lens, new, page, Hkv, H
     if fmt == "16bit":
         want, slack = rows64(k[:T], kw, rope, pos, inter)
         assert_rounded(c.at(c.k, new), want, slack, dtype)
-        assert torch.equal(c.at(c.k, new).cpu(), kd.to(dtype))     # the steps are rounded as stated
+        if not norm:
+            assert torch.equal(c.at(c.k, new).cpu(), kd.to(dtype))     # the steps are rounded as stated
         assert torch.equal(c.at(c.v, new), v[:T])
     else:
         for rows, codes, sf in ((kd, c.k, c.ks), (v[:T].float().cpu(), c.v, c.vs)):
