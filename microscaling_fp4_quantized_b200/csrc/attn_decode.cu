@@ -7,18 +7,25 @@
 // key/value head the tensor rate needed at the full memory rate is under a twentieth of the
 // chip's, so HBM is the floor.
 //
-// Work split. The tokens of all (sequence, key/value head) pairs are cut into 64-key tiles, laid
-// end to end and dealt to the CTAs in equal contiguous shares, so that neither ragged lengths nor
-// few pairs leave SMs idle. A CTA finishes the pairs that lie inside its share and leaves
-// the (at most two) that cross its borders as partial (max, sum, output) triples;
-// join_kernel adds those up in the order of the shares, so results do not depend on timing.
+// Work split. The tokens of all (sequence, key/value head) pairs are cut into tiles, laid end to
+// end and dealt to the CTAs (as many as fit the machine) in contiguous shares of equal cost, so
+// that neither ragged lengths nor few pairs leave SMs idle. A CTA finishes the pairs that lie
+// inside its share and leaves the (at most two) that cross its borders as partial (max, sum, output)
+// triples; join_kernel adds those up in the order of the shares, so results do not depend on timing.
 //
-// Each of the four warps owns 16 keys of a tile and its own ring of cp.async stages, so
-// the main loop has no block barrier; the warps meet when a pair ends. Scores are formed
-// transposed, S^T = K Q^T with 16 keys by 8 query heads per mma.m16n8k16 (a tcgen05 tile has 128 rows,
-// of which a decode step fills at most 16): a group of 8 heads wastes nothing, and movmatrix turns S^T
-// into the operand of O^T = V^T P^T. The running maximum is raised only when a score exceeds it by
+// Each of the four warps owns 16 or 32 keys of a tile and its own ring of cp.async stages, so
+// the main loop has no block barrier; the warps meet when a pair ends. Scores are formed transposed,
+// S^T = K Q^T with 16 keys by 8 query heads per mma.m16n8k16 (a tcgen05 tile has 128 rows, of which a
+// decode step fills at most 16): a group of 8 heads wastes nothing, and movmatrix turns S^T into
+// the operand of O^T = V^T P^T. The running maximum is raised only when a score exceeds it by
 // 2^4, checked by one vote per tile: probabilities then reach 2^4 times the scale they are kept at.
+//
+// Measured on one B200 with its join, share of the 6549 GB/s a copy reaches: 16-bit, 16 sequences of 256 to
+// 16384 tokens, 32 heads on 8, D 128: 98.8 us, 5.11 TB/s (0.78; torch's sum over as many contiguous bytes reads
+// 5.84 TB/s). 16-bit, 8 sequences of 2000 to 8192, 16 heads, D 64: 39.8 us, 4.2 TB/s (0.64). FP4, 64 sequences of 128 to
+// 8192, 32 heads on 8: 84.6 us, 3.86 TB/s (0.59); one sequence of 131071: 44.7 us, 3.4 TB/s (0.52). FP4 is bound by
+// the instructions that decode it, about 350 per 16 keys at 2.4 a cycle and SM (one conversion and one
+// scaling per two elements are 128 of them); the join costs 2 to 4 us of each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -35,7 +42,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWarpKeys = kTileKeys / kWarps;  // 16
 // Probabilities are kept as 2^kShift exp2(s - m): fp16 then keeps 11 bits for weights down to 2^-22
 // of the maximum, and the largest (2^kShift 2^4) is far from its limit. The factor cancels in the end.
 constexpr float kShift = 8.0f, kSlack = 4.0f;
@@ -47,6 +53,9 @@ struct Is {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool valid) {
@@ -81,31 +90,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-  return v;
-}
+// Plain shared loads (ordered by the waits before them, free to move among the arithmetic).
+__device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+__device__ __forceinline__ uint2 lds64(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ uint32_t lds16(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
+__device__ __forceinline__ uint32_t lds8(const uint8_t* p) { return *p; }
 
 // Two E4M3 bytes -> two fp16 values.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) {
@@ -124,8 +114,7 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Probabilities of two heads as one operand word, and the values that the rounding left: the
-// denominator sums those, so that the weights of the sum that is formed add up to one.
+// Weights of two heads rounded into one operand word; a and b become the rounded values.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack_p(float& a, float& b) {
   uint32_t r;
@@ -142,26 +131,30 @@ __device__ __forceinline__ uint32_t pack_p(float& a, float& b) {
   return r;
 }
 
-// Shared memory of a CTA: per warp kStages stages of 16 keys' K and V (FP4: codes of K, codes of
+// Shared memory of a CTA: per warp kStages stages of kKeys keys' K and V (FP4: codes of K, codes of
 // V, scales of K, scales of V), then the meeting area of the warps.
 template <int D, bool FP4>
 struct Smem {
+  static constexpr int kKeys = tile_keys(FP4, D) / kWarps;
   static constexpr int kKey = FP4 ? D / 2 : 2 * D;  // bytes of a key's codes or elements
   static constexpr int kSf = FP4 ? D / 16 : 0;
-  static constexpr int kV = kWarpKeys * kKey;                             // offsets in a stage
-  [[maybe_unused]] static constexpr int kKs = 2 * kV, kVs = kKs + kWarpKeys * kSf;
-  static constexpr int kStage = 2 * kWarpKeys * (kKey + kSf);
-  static constexpr int kStages = FP4 ? 4 : (D == 128 ? 3 : 4);
+  static constexpr int kV = kKeys * kKey;                                 // offsets in a stage
+  [[maybe_unused]] static constexpr int kKs = 2 * kV, kVs = kKs + kKeys * kSf;
+  static constexpr int kStage = 2 * kKeys * (kKey + kSf);
+  // Measured (us): 16-bit D = 128, 16 sequences of 256 to 16384 tokens, 8 heads: 3 stages of 16 keys and two CTAs an
+  // SM 98.8, 2 stages and three CTAs 100.9. D = 64, 8 sequences of 2000 to 8192, 16 heads: 2 stages of 32 keys and
+  // three CTAs 39.8, 3 and two 40.9. FP4, 64 sequences of 128 to 8192: 2 stages and four CTAs 91, 3 and
+  // three 97, 4 and two 112; 16 keys a warp and tile 106.
+  static constexpr int kStages = !FP4 && D == 128 ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kRow = D + 4;  // floats of a head's row in the meeting area
-  static constexpr int kMeet = kWarps * 8 * kRow * 4;
-  static constexpr int kBytes = kRing + kMeet + kWarps * 8 * 2 * 4;  // 112.8 KB at most: two CTAs per SM
+  static constexpr int kMeet = kWarps * 4 * D * 4;  // four heads at a time
+  static constexpr int kBytes = kRing + kMeet + kWarps * 8 * 2 * 4;
 };
 
 // Row of the V codes' stage that key `key` takes: a lane's keys 2t, 2t+1, 2t+8, 2t+9 lie in rows
 // t, 4+t, 8+t, 12+t, so the four lanes of a quad read consecutive rows (with the chunk
 // swizzle of D = 128, every read is free of bank conflicts).
-__device__ __forceinline__ int v_row(int key) { return (key & 8) | ((key & 1) << 2) | ((key >> 1) & 3); }
+__device__ __forceinline__ int v_row(int key) { return (key & ~7) | ((key & 1) << 2) | ((key >> 1) & 3); }
 
 // FP4 path: the query row's share of this lane (D / 4 channels from t4 * D / 4 on, two operand words per
 // step of four) in fp16. The row is scaled by a power of two that brings its maximum into [2^14, 2^15),
@@ -205,14 +198,14 @@ __device__ __forceinline__ void load_q_fp16(const T* q, bool valid, int t4, uint
 // (r, t4) takes channels t4 D/4 .. of keys r and r + 8, one or two whole scale blocks, and
 // step k contracts channels 4k .. 4k+3 of each lane's range.
 template <int D, int NT>
-__device__ __forceinline__ void scores_fp4(uint32_t stage, int r, int t4, const uint32_t (&qf)[NT][D / 16][2], float (&s)[NT][4]) {
+__device__ __forceinline__ void scores_fp4(const uint8_t* stage, int k0, int r, int t4, const uint32_t (&qf)[NT][D / 16][2], float (&s)[NT][4]) {
   using S = Smem<D, true>;
   constexpr int W = D / 32;  // code words of a lane and key: 4 or 2
   uint32_t w[2][W], sc[2];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    const int key = r + 8 * half;
-    const uint32_t sf = stage + S::kKs + key * S::kSf;
+    const int key = k0 + r + 8 * half;
+    const uint8_t* sf = stage + S::kKs + key * S::kSf;
     if constexpr (D == 128) {
       const uint4 v = lds128(stage + key * S::kKey + t4 * 16);
       w[half][0] = v.x; w[half][1] = v.y; w[half][2] = v.z; w[half][3] = v.w;
@@ -244,13 +237,13 @@ __device__ __forceinline__ void scores_fp4(uint32_t stage, int r, int t4, const 
 // the operand wants two keys' values of one channel side by side, so the nibbles of two
 // keys are interleaved before they are decoded.
 template <int D, int NT>
-__device__ __forceinline__ void values_fp4(uint32_t stage, int r, int t4, const uint32_t (&pb)[NT][2], float (&o)[NT][D / 16][4]) {
+__device__ __forceinline__ void values_fp4(const uint8_t* stage, int k0, int r, int t4, const uint32_t (&pb)[NT][2], float (&o)[NT][D / 16][4]) {
   using S = Smem<D, true>;
   constexpr int W = D / 64;  // code words of a lane and key: 2 or 1
   uint32_t w[4][W], sc[2];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const uint32_t row = stage + S::kV + (4 * e + t4) * S::kKey;
+    const uint8_t* row = stage + S::kV + (k0 + 4 * e + t4) * S::kKey;
     if constexpr (D == 128) {
       const uint2 v = lds64(row + (((r >> 1) ^ (t4 & 2)) << 4) + (r & 1) * 8);
       w[e][0] = v.x; w[e][1] = v.y;
@@ -260,7 +253,7 @@ __device__ __forceinline__ void values_fp4(uint32_t stage, int r, int t4, const 
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t sf = stage + S::kVs + (8 * h + 2 * t4) * S::kSf + (D == 128 ? r : r >> 1);
+    const uint8_t* sf = stage + S::kVs + (k0 + 8 * h + 2 * t4) * S::kSf + (D == 128 ? r : r >> 1);
     sc[h] = e4m3x2_to_f16x2(lds8(sf) | lds8(sf + S::kSf) << 8);
   }
 #pragma unroll
@@ -297,11 +290,19 @@ __device__ __forceinline__ void store_out(T* out, const float (&acc)[N], float s
     }
   }
   if constexpr (N == 8) *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-  else *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  else if constexpr (N == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(out) = w[0];
 }
 
+// What a pair costs besides its tiles (its queries, the meeting of the warps), in tiles. Measured on
+// the ragged FP4 batch (us): 0 91.6, 1 84.6, 2 84.0, 3 85.8; on one long sequence 44.7, 44.9, 45.2, 45.6.
+constexpr int kPairCost = 1;
+
 // Tiles of a sequence: at least one, so that empty sequences too get their (zero) output.
-__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTileKeys - 1) / kTileKeys : 1; }
+template <bool FP4, int D>
+__device__ __forceinline__ int tiles_of(int len) {
+  return len > 0 ? (len + tile_keys(FP4, D) - 1) / tile_keys(FP4, D) : 1;
+}
 
 __device__ __forceinline__ int length_of(const CacheView& c, int b, uint32_t* err) {
   const int len = __ldg(c.lens + b);
@@ -310,13 +311,14 @@ __device__ __forceinline__ int length_of(const CacheView& c, int b, uint32_t* er
   return len < 0 ? 0 : c.capacity;
 }
 
-// Tiles of all sequences (of one head chunk), and in `mine` those before this thread's range of
+// Cost of all sequences (of one head chunk), and in `mine` of those before this thread's range of
 // ceil(B / kThreads) sequences; by the whole block.
+template <bool FP4, int D>
 __device__ __forceinline__ int64_t count_tiles(const CacheView& c, int64_t* red, int64_t* mine, uint32_t* err) {
   const int per = (c.B + kThreads - 1) / kThreads, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int lo = min(c.B, static_cast<int>(threadIdx.x) * per), hi = min(c.B, lo + per);
   int64_t s = 0;
-  for (int b = lo; b < hi; ++b) s += tiles_of(length_of(c, b, err));
+  for (int b = lo; b < hi; ++b) s += tiles_of<FP4, D>(length_of(c, b, err)) + kPairCost;
   int64_t inc = s;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -338,45 +340,41 @@ __device__ __forceinline__ int64_t count_tiles(const CacheView& c, int64_t* red,
 // First tile of CTA i's share of W tiles.
 __device__ __forceinline__ int64_t share(int64_t W, int i, int grid) { return W * i / grid; }
 
-// Place in the row of tiles: sequence, head chunk, tile.
+// Place in the row of tiles: sequence, key/value head, chunk of its query heads, tile; `at` counts costs from
+// the share's beginning.
 struct Cursor {
-  int b, hc, t, len, nt;
+  int b, hk, chunk, t, len, nt, at;
 };
 
 }  // namespace
 
 template <typename T, int D, int NT, bool FP4>
-__global__ void __launch_bounds__(kThreads, FP4 && NT == 1 ? 4 : 2) decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2 : 3) decode_kernel(const DecodeParams p) {
   using S = Smem<D, FP4>;
   constexpr bool kMmaBf16 = Is<T>::bf16 && !FP4;  // FP4 values are exact in fp16
   constexpr int KS = D / 16;                      // contraction steps of S^T, channel tiles of O^T
+  constexpr int KW = S::kKeys, G = KW / 16;       // keys of a warp and tile, in groups of 16
   extern __shared__ __align__(16) uint8_t smem[];
   float* meet = reinterpret_cast<float*>(smem + S::kRing);
-  float* meet_ml = meet + kWarps * 8 * S::kRow;
+  float* meet_ml = meet + kWarps * 4 * D;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, t4 = lane & 3;
   const CacheView& c = p.c;
   const int HC = c.Hkv * p.chunks;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // join_kernel may be launched: it waits for the end
 
   // This CTA's share, and where it begins.
   int64_t before;
   __shared__ int64_t s_red[kWarps];
   __shared__ int s_b;
   __shared__ int64_t s_before;
-  const int64_t W = count_tiles(c, s_red, &before, blockIdx.x == 0 ? p.err : nullptr) * HC;
+  const int64_t W = count_tiles<FP4, D>(c, s_red, &before, blockIdx.x == 0 ? p.err : nullptr) * HC;
   const int64_t u0 = share(W, blockIdx.x, p.grid), u1 = share(W, blockIdx.x + 1, p.grid);
-  if (u0 >= u1) {  // uniform over the block. Fewer tiles than CTAs: a join skips the empty shares
-    if (tid < 8 * NT) {
-      float* ml = p.part_ml + (static_cast<int64_t>(blockIdx.x) * 2 * (8 * NT) + tid) * 2;
-      ml[0] = -INFINITY;
-      ml[1] = 0.0f;
-    }
-    return;
-  }
   {
     const int per = (c.B + kThreads - 1) / kThreads;
     const int lo = min(c.B, tid * per), hi = min(c.B, lo + per);
     for (int b = lo; b < hi; ++b) {
-      const int64_t n = tiles_of(length_of(c, b, nullptr));
+      const int64_t n = tiles_of<FP4, D>(length_of(c, b, nullptr)) + kPairCost;
       if (before * HC <= u0 && u0 < (before + n) * HC) {
         s_b = b;
         s_before = before;
@@ -385,31 +383,51 @@ __global__ void __launch_bounds__(kThreads, FP4 && NT == 1 ? 4 : 2) decode_kerne
     }
   }
   __syncthreads();
+  const bool by_pair = p.joins < p.grid;  // (see the records below)
+  const int span = static_cast<int>(u1 - u0);
   Cursor pc;  // where the copies are
-  pc.b = s_b;
-  pc.len = length_of(c, pc.b, nullptr);
-  pc.nt = tiles_of(pc.len);
-  {
+  pc.at = 0;
+  if (span > 0) {
+    pc.b = s_b;
+    pc.len = length_of(c, pc.b, nullptr);
+    pc.nt = tiles_of<FP4, D>(pc.len);
     const int64_t in = u0 - s_before * HC;
-    pc.hc = static_cast<int>(in / pc.nt);
-    pc.t = static_cast<int>(in - static_cast<int64_t>(pc.hc) * pc.nt);
+    const int hc = static_cast<int>(in / (pc.nt + kPairCost));
+    const int rest = static_cast<int>(in - static_cast<int64_t>(hc) * (pc.nt + kPairCost)) - kPairCost;
+    pc.t = max(rest, 0);
+    pc.at = max(-rest, 0);
+    pc.hk = hc / p.chunks;
+    pc.chunk = hc - pc.hk * p.chunks;
+  }
+  if (pc.at >= span) {  // no tile in this share (uniform over the block): a join skips it
+    if (tid < 8 * NT) {
+      float* ml = p.part_ml + (static_cast<int64_t>(blockIdx.x) * 2 * (8 * NT) + tid) * 2;
+      ml[0] = -INFINITY;
+      ml[1] = 0.0f;
+    }
+    if (tid == 0 && !by_pair) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
   }
   Cursor cc = pc;  // where the arithmetic is
-  const int count = static_cast<int>(u1 - u0);
 
   auto advance = [&](Cursor& x) {
+    ++x.at;
     if (++x.t < x.nt) return;
+    x.at += kPairCost;
     x.t = 0;
-    if (++x.hc < HC) return;
-    x.hc = 0;
+    if (++x.chunk < p.chunks) return;
+    x.chunk = 0;
+    if (++x.hk < c.Hkv) return;
+    x.hk = 0;
     if (++x.b < c.B) {
       x.len = length_of(c, x.b, nullptr);
-      x.nt = tiles_of(x.len);
+      x.nt = tiles_of<FP4, D>(x.len);
     }
   };
-  // The page of this lane's key (lanes 0-15: for K, 16-31: the same keys, for V), loaded one tile ahead.
+  const int my_key = warp * KW + lane % KW;  // of a tile; 16-bit: lanes 16 apart hold the same key
+  // The page of this lane's key, loaded one tile ahead (-1: no such key, or no such page).
   auto page_of = [&](const Cursor& x) -> int {
-    const int pos = x.t * kTileKeys + warp * kWarpKeys + (lane & 15);
+    const int pos = x.t * tile_keys(FP4, D) + my_key;
     if (pos >= x.len) return -1;
     const int page = __ldg(c.table + x.b * c.table_stride + div_by_page(c.page, pos));
     if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(c.num_pages)) {
@@ -419,69 +437,69 @@ __global__ void __launch_bounds__(kThreads, FP4 && NT == 1 ? 4 : 2) decode_kerne
     return page;
   };
   const uint32_t ring = smem_u32(smem) + warp * (S::kStages * S::kStage);
-  const Strides st = lane < 16 ? c.sk : c.sv;
-  auto copy_tile = [&](const Cursor& x, int page, uint32_t stage) {
-    const int k0 = x.t * kTileKeys + warp * kWarpKeys;
-    if (k0 >= x.len) return;
-    // Lane l's key as a row offset in units of 16 bytes; bit-all-ones: no such key.
-    const uint32_t pos = k0 + (lane & 15);
-    const uint32_t slot = pos - div_by_page(c.page, pos) * c.page.d;
-    uint32_t off = 0xffffffffu;
-    if (page >= 0) {
-      const int64_t el = page * st.b + static_cast<int64_t>(x.hc / p.chunks) * st.h + static_cast<int64_t>(slot) * st.n;
-      off = static_cast<uint32_t>(el / (FP4 ? 32 : 8));
-    }
-    constexpr int CPK = S::kKey / 16, KPI = 32 / CPK;  // 16-byte chunks per key, keys per instruction
-    const int ch = lane % CPK;
+  constexpr int CPK = S::kKey / 16, KPI = 32 / CPK;  // 16-byte chunks per key, keys per copy instruction
+  const int ch = lane % CPK, kk = lane / CPK;
+  const char* const k_src = static_cast<const char*>(c.k) + ch * 16;
+  const char* const v_src = static_cast<const char*>(c.v) + ch * 16;
+  const uint32_t k_at = FP4 ? kk * S::kKey + (ch << 4) : kk * S::kKey + ((ch ^ (kk & 7)) << 4);
+  const uint32_t v_at = !FP4 ? k_at : v_row(kk) * S::kKey + ((D == 128 ? ch ^ (v_row(kk) & 2) : ch) << 4);
+  auto copy_rows = [&](uint32_t ko, uint32_t vo, uint32_t stage, auto all) {
+    // ALL: every key is there, so the copies need no length of their own.
+    constexpr bool ALL = decltype(all)::value;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const char* base = static_cast<const char*>(half ? c.v : c.k);
-      const uint32_t dst = stage + half * S::kV;
+      const uint32_t lane_at = half ? v_at : k_at;
 #pragma unroll
-      for (int i = 0; i < kWarpKeys / KPI; ++i) {
-        const int key = i * KPI + lane / CPK;
-        const uint32_t o = __shfl_sync(0xffffffffu, off, half * 16 + key);
-        const bool valid = o != 0xffffffffu;
-        uint32_t at;
-        if constexpr (!FP4) {
-          at = key * S::kKey + ((ch ^ (key & 7)) << 4);
-        } else if (half == 0) {
-          at = key * S::kKey + (ch << 4);
-        } else {
-          const int row = v_row(key);
-          at = row * S::kKey + ((D == 128 ? ch ^ (row & 2) : ch) << 4);
-        }
-        cp_async16(dst + at, base + (valid ? static_cast<uint64_t>(o) * 16 : 0) + ch * 16, valid);
+      for (int i = 0; i < KW / KPI; ++i) {
+        const uint32_t o = __shfl_sync(0xffffffffu, half ? vo : ko, i * KPI + kk);
+        const bool valid = ALL || o != 0xffffffffu;
+        // 16-bit: the part of the swizzle that i brings flips chunk bits (rows are multiples of 128 bytes)
+        const uint32_t at = stage + (FP4 ? lane_at : lane_at ^ (((KPI * i) & 7) << 4)) + half * S::kV + i * KPI * S::kKey;
+        const char* src = (half ? v_src : k_src) + static_cast<uint64_t>(valid ? o : 0u) * 16;
+        if constexpr (ALL) cp_async16(at, src);
+        else cp_async16(at, src, valid);
       }
     }
     if constexpr (FP4) {
-      const bool valid = off != 0xffffffffu;
-      const uint8_t* sf = lane < 16 ? c.k_sf : c.v_sf;
-      cp_async_small<S::kSf>(stage + S::kKs + lane * S::kSf, sf + (valid ? static_cast<uint64_t>(off) * 2 : 0), valid);
+      const bool valid = ALL || ko != 0xffffffffu;
+      cp_async_small<S::kSf>(stage + S::kKs + lane * S::kSf, c.k_sf + static_cast<uint64_t>(valid ? ko : 0u) * 2, valid);
+      cp_async_small<S::kSf>(stage + S::kVs + lane * S::kSf, c.v_sf + static_cast<uint64_t>(valid ? vo : 0u) * 2, valid);
     }
+  };
+  auto copy_tile = [&](const Cursor& x, int page, uint32_t stage) {
+    if (x.t * tile_keys(FP4, D) + warp * KW >= x.len) return;
+    // This lane's key as row offsets in units of 16 bytes; all ones: no such key.
+    const uint32_t pos = x.t * tile_keys(FP4, D) + my_key;
+    const uint32_t slot = pos - div_by_page(c.page, pos) * c.page.d;
+    const uint32_t ko = page * p.ku[0] + x.hk * p.ku[1] + slot * p.ku[2];
+    const uint32_t vo = page * p.vu[0] + x.hk * p.vu[1] + slot * p.vu[2];
+    if (__all_sync(0xffffffffu, page >= 0)) copy_rows(ko, vo, stage, std::true_type{});
+    else copy_rows(page >= 0 ? ko : 0xffffffffu, page >= 0 ? vo : 0xffffffffu, stage, std::false_type{});
   };
 
   int page = page_of(pc);
 #pragma unroll
   for (int i = 0; i < S::kStages - 1; ++i) {
-    if (i < count) {
+    if (pc.at < span) {
       copy_tile(pc, page, ring + i * S::kStage);
       advance(pc);
-      if (i + 1 < count) page = page_of(pc);
+      if (pc.at < span) page = page_of(pc);
     }
     cp_async_commit();
   }
 
   uint32_t qf[NT][KS][2];
-  float o[NT][KS][4], m[NT][2], l[NT][2], qs[NT][2];
+  // Per head column: the running maximum m (of scaled scores), the unscaled score that makes it rise, and the
+  // offset of the exponent.
+  float o[NT][KS][4], m[NT][2], rise[NT][2], shift[NT][2], l[NT][2], qs[NT][2];
   uint32_t slot = 0, fill = S::kStages - 1;  // stages to read and to refill
   bool first = true;
-  for (int i = 0; i < count; ++i) {
-    const int hk = cc.hc / p.chunks, chunk = cc.hc - hk * p.chunks;
-    const int head0 = hk * p.group + chunk * p.chunk_heads;
-    const int heads = min(p.chunk_heads, p.group - chunk * p.chunk_heads);
+  int head0 = 0, heads = 0;
+  while (cc.at < span) {
     if (first) {  // a new pair: its queries
       first = false;
+      head0 = cc.hk * p.group + cc.chunk * p.chunk_heads;
+      heads = min(p.chunk_heads, p.group - cc.chunk * p.chunk_heads);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int h = n * 8 + r;
@@ -497,10 +515,13 @@ __global__ void __launch_bounds__(kThreads, FP4 && NT == 1 ? 4 : 2) decode_kerne
         } else {
           load_q_fp16<T, KS>(q, h < heads, t4, qf[n], sc);
         }
-        qs[n][0] = p.scale_log2 * sc[0];
-        qs[n][1] = p.scale_log2 * sc[1];
-        m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          qs[n][e] = fmaxf(p.scale_log2 * sc[e], 1.2e-38f);  // never 0: masked scores stay -inf
+          m[n][e] = rise[n][e] = -INFINITY;
+          shift[n][e] = -kShift;
+          l[n][e] = 0.0f;
+        }
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -509,52 +530,69 @@ __global__ void __launch_bounds__(kThreads, FP4 && NT == 1 ? 4 : 2) decode_kerne
     }
     cp_async_wait<S::kStages - 2>();
     __syncwarp();  // this tile has arrived for every lane, and every lane has read the one before
-    if (i + S::kStages - 1 < count) {
+    if (pc.at < span) {
       copy_tile(pc, page, ring + fill * S::kStage);
       advance(pc);
-      if (i + S::kStages < count) page = page_of(pc);
+      if (pc.at < span) page = page_of(pc);
     }
     cp_async_commit();
-    const int k0 = cc.t * kTileKeys + warp * kWarpKeys;
+    const int k0 = cc.t * tile_keys(FP4, D) + warp * KW;
     if (k0 < cc.len) {
       const uint32_t stage = ring + slot * S::kStage;
-      float s[NT][4];
+      [[maybe_unused]] const uint8_t* stage_p = smem + warp * (S::kStages * S::kStage) + slot * S::kStage;
+      float s[G][NT][4];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[g][n][e] = 0.0f;
+        if constexpr (!FP4) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const int key = 16 * g + (lane & 7) + (lane & 8), c2 = 2 * k + (lane >> 4);
+            uint32_t a[4];
+            ldsm4(stage + key * S::kKey + ((c2 ^ (key & 7)) << 4), a);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<kMmaBf16>(s[g][n], a, qf[n][k][0], qf[n][k][1]);
+          }
+        } else {
+          scores_fp4<D, NT>(stage_p, 16 * g, r, t4, qf, s[g]);
+        }
+      }
+      if (k0 + KW > cc.len) {  // the sequence ends in here
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (k0 + 16 * g + (e < 2 ? 0 : 8) + r >= cc.len) s[g][n][e] = -INFINITY;
+      }
+      float top[NT][2];
+      bool raise = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-      if constexpr (!FP4) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const int key = (lane & 7) + (lane & 8), ch = 2 * k + (lane >> 4);
-          uint32_t a[4];
-          ldsm4(stage + key * S::kKey + ((ch ^ (key & 7)) << 4), a);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<kMmaBf16>(s[n], a, qf[n][k][0], qf[n][k][1]);
+        for (int e = 0; e < 2; ++e) {
+          top[n][e] = fmaxf(s[0][n][e], s[0][n][e + 2]);
+          if (G == 2) top[n][e] = fmaxf(top[n][e], fmaxf(s[G - 1][n][e], s[G - 1][n][e + 2]));
+          raise |= top[n][e] > rise[n][e];
         }
-      } else {
-        scores_fp4<D, NT>(stage, r, t4, qf, s);
-      }
-      const bool ok0 = k0 + r < cc.len, ok1 = k0 + 8 + r < cc.len;
-      bool raise = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = (e < 2 ? ok0 : ok1) ? s[n][e] * qs[n][e & 1] : -INFINITY;
-        raise |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kSlack || fmaxf(s[n][1], s[n][3]) > m[n][1] + kSlack;
-      }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(s[n][e], s[n][e + 2]);
+            float x = top[n][e];
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x, m[n][e]);
+            x = fmaxf(x * qs[n][e], m[n][e]);
             const float f = m[n][e] == -INFINITY ? 0.0f : ex2_approx(m[n][e] - x);
             m[n][e] = x;
+            rise[n][e] = (x + kSlack) / qs[n][e];
+            shift[n][e] = (x == -INFINITY ? 0.0f : x) - kShift;
             l[n][e] *= f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -563,32 +601,48 @@ __global__ void __launch_bounds__(kThreads, FP4 && NT == 1 ? 4 : 2) decode_kerne
             }
           }
       }
-      uint32_t pb[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int g = 0; g < G; ++g) {
+        // Weights as operands. 16-bit: the rounded weight and, in an operand of its own, what the rounding left (the
+        // tensor cores have room: one rounding of bf16 alone is as large as the output's). FP4: fp16's 11
+        // bits are well below the cache's own rounding; the sum then takes the rounded weights.
+        uint32_t pb[NT][2];
+        [[maybe_unused]] uint32_t pl[NT][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1];
-          s[n][e] = ex2_approx(s[n][e] - ref + kShift);
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[g][n][e] = ex2_approx(fmaf(s[g][n][e], qs[n][e & 1], -shift[n][e & 1]));
+          float h[4] = {s[g][n][0], s[g][n][1], s[g][n][2], s[g][n][3]};
+          pb[n][0] = movm_t(pack_p<kMmaBf16>(h[0], h[1]));
+          pb[n][1] = movm_t(pack_p<kMmaBf16>(h[2], h[3]));
+          if constexpr (!FP4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h[e] = s[g][n][e] - h[e];
+            }
+            pl[n][0] = movm_t(pack_p<kMmaBf16>(h[0], h[1]));
+            pl[n][1] = movm_t(pack_p<kMmaBf16>(h[2], h[3]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = s[g][n][e];
+          }
+          l[n][0] += h[0] + h[2];
+          l[n][1] += h[1] + h[3];
         }
-        pb[n][0] = pack_p<kMmaBf16>(s[n][0], s[n][1]);
-        pb[n][1] = pack_p<kMmaBf16>(s[n][2], s[n][3]);
-        l[n][0] += s[n][0] + s[n][2];
-        l[n][1] += s[n][1] + s[n][3];
-        pb[n][0] = movm_t(pb[n][0]);
-        pb[n][1] = movm_t(pb[n][1]);
-      }
-      if constexpr (!FP4) {
+        if constexpr (!FP4) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const int key = (lane & 7) + ((lane & 16) >> 1), ch = 2 * k + ((lane >> 3) & 1);
-          uint32_t a[4];
-          ldsm4_t(stage + S::kV + key * S::kKey + ((ch ^ (key & 7)) << 4), a);
+          for (int k = 0; k < KS; ++k) {
+            const int key = 16 * g + (lane & 7) + ((lane & 16) >> 1), c2 = 2 * k + ((lane >> 3) & 1);
+            uint32_t a[4];
+            ldsm4_t(stage + S::kV + key * S::kKey + ((c2 ^ (key & 7)) << 4), a);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<kMmaBf16>(o[n][k], a, pb[n][0], pb[n][1]);
+            for (int n = 0; n < NT; ++n) {
+              mma16816<kMmaBf16>(o[n][k], a, pb[n][0], pb[n][1]);
+              mma16816<kMmaBf16>(o[n][k], a, pl[n][0], pl[n][1]);
+            }
+          }
+        } else {
+          values_fp4<D, NT>(stage_p, 16 * g, r, t4, pb, o);
         }
-      } else {
-        values_fp4<D, NT>(stage, r, t4, pb, o);
       }
     }
     slot = slot + 1 == S::kStages ? 0 : slot + 1;
@@ -596,24 +650,21 @@ __global__ void __launch_bounds__(kThreads, FP4 && NT == 1 ? 4 : 2) decode_kerne
 
     const Cursor at = cc;
     advance(cc);
-    if (at.t + 1 < at.nt && i + 1 < count) continue;
+    if (at.t + 1 < at.nt && cc.at < span) continue;
     // The pair ends, here or with this share: the warps meet.
     first = true;
-    const bool whole = at.t + 1 == at.nt && at.t <= i;  // its first tile was tile i - at.t of this share
+    const bool begun = at.at >= at.t, whole = begun && at.t + 1 == at.nt;
     // Partial 0: a pair that began before this share; partial 1: one that only goes on after it.
-    const int part = at.t > i ? 0 : 1;
-    if (tid == 0) {
+    const int part = begun ? 1 : 0;
+    if (tid == 0 && (by_pair ? begun : cc.at >= span)) {
       // What join_kernel has to do, one record per pair (by the CTA with the pair's first tile) or, when
       // there are more pairs than CTAs, one per CTA (for the pair that goes on after it).
-      const bool by_pair = p.joins < p.grid;
-      if (by_pair ? part == 1 : i + 1 == count) {
-        int4 rec = make_int4(-1, 0, 0, 0);
-        if (part == 1 && !whole) {
-          const int64_t end = u0 + i - at.t + at.nt;  // past the pair's last tile
-          rec = make_int4(at.b, at.hc, static_cast<int>(blockIdx.x), static_cast<int>((end * p.grid - 1) / W));
-        }
-        p.rec[by_pair ? static_cast<int64_t>(at.b) * HC + at.hc : blockIdx.x] = rec;
+      int4 rec = make_int4(-1, 0, 0, 0);
+      if (begun && !whole) {
+        const int64_t end = u0 + at.at - at.t + at.nt;  // past the pair's last tile
+        rec = make_int4(at.b, at.hk * p.chunks + at.chunk, static_cast<int>(blockIdx.x), static_cast<int>((end * p.grid - 1) / W));
       }
+      p.rec[by_pair ? static_cast<int64_t>(at.b) * HC + at.hk * p.chunks + at.chunk : blockIdx.x] = rec;
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -623,61 +674,65 @@ __global__ void __launch_bounds__(kThreads, FP4 && NT == 1 ? 4 : 2) decode_kerne
         l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
         l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
       }
-      __syncthreads();  // the area's last readers are done
-      if (r == 0) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          meet_ml[(warp * 8 + 2 * t4 + e) * 2] = m[n][e];
-          meet_ml[(warp * 8 + 2 * t4 + e) * 2 + 1] = l[n][e];
+      for (int pass = 0; pass < 2; ++pass) {  // heads 0-3, then 4-7
+        if (n * 8 + pass * 4 >= heads) break;  // uniform over the block
+        __syncthreads();                       // the area's last readers are done
+        if (r == 0 && pass == 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            meet_ml[(warp * 8 + 2 * t4 + e) * 2] = m[n][e];
+            meet_ml[(warp * 8 + 2 * t4 + e) * 2 + 1] = l[n][e];
+          }
         }
-      }
-      float* row = meet + (warp * 8 + 2 * t4) * S::kRow;
+        if ((t4 >> 1) == pass) {
+          float* row = meet + (warp * 4 + 2 * (t4 & 1)) * D;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        // Channels of a tile's two rows: neighbours of the lane's own range in FP4, else 8 apart.
-        const int ch = FP4 ? (D / 8) * r + 2 * k : 16 * k + r;
-        constexpr int step = FP4 ? 1 : 8;
-        row[ch] = o[n][k][0];
-        row[S::kRow + ch] = o[n][k][1];
-        row[ch + step] = o[n][k][2];
-        row[S::kRow + ch + step] = o[n][k][3];
-      }
-      __syncthreads();
-      // 16 threads per head, D / 16 channels each.
-      const int h = tid >> 4, c0 = (tid & 15) * (D / 16);
-      float mx = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, meet_ml[(w * 8 + h) * 2]);
-      float acc[D / 16], sum = 0.0f;
-#pragma unroll
-      for (int e = 0; e < D / 16; ++e) acc[e] = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = meet_ml[(w * 8 + h) * 2];
-        const float f = mw == -INFINITY ? 0.0f : ex2_approx(mw - mx);
-        sum += meet_ml[(w * 8 + h) * 2 + 1] * f;
-        const float* src = meet + (w * 8 + h) * S::kRow + c0;
-#pragma unroll
-        for (int e = 0; e < D / 16; e += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src + e);
-          acc[e] += v.x * f;
-          acc[e + 1] += v.y * f;
-          acc[e + 2] += v.z * f;
-          acc[e + 3] += v.w * f;
+          for (int k = 0; k < KS; ++k) {
+            // Channels of a tile's two rows: neighbours of the lane's own range in FP4, else 8 apart.
+            const int ch = FP4 ? (D / 8) * r + 2 * k : 16 * k + r;
+            constexpr int step = FP4 ? 1 : 8;
+            row[ch] = o[n][k][0];
+            row[D + ch] = o[n][k][1];
+            row[ch + step] = o[n][k][2];
+            row[D + ch + step] = o[n][k][3];
+          }
         }
-      }
-      if (n * 8 + h < heads) {
-        if (whole) {
-          T* out = static_cast<T*>(p.out) + at.b * p.sob + static_cast<int64_t>(head0 + n * 8 + h) * p.soh + c0;
-          store_out<T, D / 16>(out, acc, sum);
-        } else {
-          const int64_t g = (static_cast<int64_t>(blockIdx.x) * 2 + part) * (8 * NT) + n * 8 + h;
-          float* po = p.part_o + g * D + c0;
+        __syncthreads();
+        // 32 threads per head, D / 32 channels each.
+        constexpr int N = D / 32;
+        const int hh = tid >> 5, h = pass * 4 + hh, c0 = (tid & 31) * N;
+        float mx = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < D / 16; e += 4) *reinterpret_cast<float4*>(po + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-          if ((tid & 15) == 0) {
-            p.part_ml[g * 2] = mx;
-            p.part_ml[g * 2 + 1] = sum;
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, meet_ml[(w * 8 + h) * 2]);
+        float acc[N], sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = meet_ml[(w * 8 + h) * 2];
+          const float f = mw == -INFINITY ? 0.0f : ex2_approx(mw - mx);
+          sum += meet_ml[(w * 8 + h) * 2 + 1] * f;
+          const float2* src = reinterpret_cast<const float2*>(meet + (w * 4 + hh) * D + c0);
+#pragma unroll
+          for (int e = 0; e < N; e += 2) {
+            acc[e] += src[e / 2].x * f;
+            acc[e + 1] += src[e / 2].y * f;
+          }
+        }
+        if (n * 8 + h < heads) {
+          if (whole) {
+            T* out = static_cast<T*>(p.out) + at.b * p.sob + static_cast<int64_t>(head0 + n * 8 + h) * p.soh + c0;
+            store_out<T, N>(out, acc, sum);
+          } else {
+            const int64_t g = (static_cast<int64_t>(blockIdx.x) * 2 + part) * (8 * NT) + n * 8 + h;
+            float2* po = reinterpret_cast<float2*>(p.part_o + g * D + c0);
+#pragma unroll
+            for (int e = 0; e < N; e += 2) po[e / 2] = make_float2(acc[e], acc[e + 1]);
+            if ((tid & 31) == 0) {
+              p.part_ml[g * 2] = mx;
+              p.part_ml[g * 2 + 1] = sum;
+            }
           }
         }
       }
@@ -699,26 +754,39 @@ __global__ void __launch_bounds__(128) join_kernel(const DecodeParams p) {
   const int hk = rec.y / p.chunks, chunk = rec.y - hk * p.chunks;
   if (h >= min(p.chunk_heads, p.group - chunk * p.chunk_heads)) return;
   auto row_of = [&](int cta) { return (static_cast<int64_t>(cta) * 2 + (cta == rec.z ? 1 : 0)) * (8 * NT) + h; };
-  // The group's maximum first: the sums then need no rescaling.
-  float mx = -INFINITY;
-  for (int cta = rec.z + g; cta <= rec.w; cta += 8) mx = fmaxf(mx, p.part_ml[row_of(cta) * 2]);
-  float acc[N], sum = 0.0f;
+  float mx = -INFINITY, acc[N], sum = 0.0f;
 #pragma unroll
   for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-  for (int cta = rec.z + g; cta <= rec.w; cta += 8) {
-    const int64_t row = row_of(cta);
-    const float m = p.part_ml[row * 2];
-    if (m == -INFINITY) continue;  // an empty share has no output
-    const float f = ex2_approx(m - mx);
-    sum += p.part_ml[row * 2 + 1] * f;
+  constexpr int U = 4;  // partials loaded together, before their maxima are known
+  for (int first = rec.z + g; first <= rec.w; first += 8 * U) {
+    float m[U], l[U];
+    float4 v[U][N / 4];
 #pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + row * D + c0 + e);
-      acc[e] += v.x * f;
-      acc[e + 1] += v.y * f;
-      acc[e + 2] += v.z * f;
-      acc[e + 3] += v.w * f;
+    for (int u = 0; u < U; ++u) {
+      m[u] = -INFINITY;
+      if (first + 8 * u <= rec.w) {
+        const int64_t row = row_of(first + 8 * u);
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + row * 2);
+        m[u] = ml.x;
+        l[u] = ml.y;
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) v[u][e] = *reinterpret_cast<const float4*>(p.part_o + row * D + c0 + 4 * e);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (m[u] == -INFINITY) continue;  // none, or an empty share, which has no output
+      const float top = fmaxf(mx, m[u]);
+      const float f0 = mx == -INFINITY ? 0.0f : ex2_approx(mx - top), f1 = ex2_approx(m[u] - top);
+      mx = top;
+      sum = sum * f0 + l[u] * f1;
+#pragma unroll
+      for (int e = 0; e < N / 4; ++e) {
+        acc[4 * e] = acc[4 * e] * f0 + v[u][e].x * f1;
+        acc[4 * e + 1] = acc[4 * e + 1] * f0 + v[u][e].y * f1;
+        acc[4 * e + 2] = acc[4 * e + 2] * f0 + v[u][e].z * f1;
+        acc[4 * e + 3] = acc[4 * e + 3] * f0 + v[u][e].w * f1;
+      }
     }
   }
 #pragma unroll
@@ -788,7 +856,7 @@ cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   p.joins = static_cast<int>(pairs < p.grid ? pairs : p.grid);
   decode_kernel<T, D, NT, FP4><<<p.grid, kThreads, smem, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.c.capacity <= kTileKeys) return cudaSuccess;  // one tile per pair: none is split
+  if (p.c.capacity <= tile_keys(FP4, D)) return cudaSuccess;  // one tile per pair: none is split
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.joins, p.chunk_heads);
   cfg.blockDim = dim3(128);

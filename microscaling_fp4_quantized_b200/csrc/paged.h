@@ -77,6 +77,7 @@ struct DecodeParams {
   int chunk_heads;     // query heads of a chunk (the last one may have fewer)
   float scale_log2;    // sm_scale * log2(e)
   CacheView c;
+  uint32_t ku[3], vu[3];  // strides of (page, head, slot) in units of 16 bytes of codes or elements
   float* part_o;       // [grid, 2, 8 * NT, D]
   float* part_ml;      // [grid, 2, 8 * NT, 2]
   int4* rec;           // [joins] what is to be joined
@@ -84,7 +85,8 @@ struct DecodeParams {
   uint32_t* err;
 };
 
-constexpr int kTileKeys = 64;       // keys of a CTA tile of the decode kernel
+// Keys of a CTA tile of the decode kernel: four warps with 16 (16-bit, D = 128) or 32 each.
+__host__ __device__ constexpr int tile_keys(bool fp4, int D) { return fp4 ? 128 : D == 64 ? 128 : 64; }
 constexpr int kMaxDecodeCtas = 1184;  // 8 per SM: bound of the decode grid and of its workspace
 
 cudaError_t launch_rows(const RowsParams& p, int D, int dtype, bool to_cache, bool fp4, cudaStream_t stream);

@@ -147,9 +147,10 @@ sage_status_t plan_decode(const sage_fp4_cache_t* c, const sage_fp4_batch_t* b, 
   d->NT = d->chunk_heads > 8 ? 2 : 1;
   const int64_t pairs = static_cast<int64_t>(b->B) * c->Hkv * d->chunks;
   if (pairs >= (int64_t(1) << 26) || Hq > 65535) return SAGE_ERR_UNSUPPORTED;
-  const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(b->table_width) * c->page_size + sage::kTileKeys - 1) / sage::kTileKeys);
+  const int tile = sage::tile_keys(c->format == SAGE_CACHE_FP4, c->D);
+  const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(b->table_width) * c->page_size + tile - 1) / tile);
   if (tiles * pairs >= (int64_t(1) << 38)) return SAGE_ERR_UNSUPPORTED;  // a share's tiles are counted in 32 bits
-  d->max_grid = static_cast<int>(std::min<int64_t>(sage::kMaxDecodeCtas, pairs * tiles));
+  d->max_grid = static_cast<int>(std::min<int64_t>(sage::kMaxDecodeCtas, pairs * (tiles + 1)));
   const size_t rows = static_cast<size_t>(d->max_grid) * 2 * 8 * d->NT;
   d->rec = up256(static_cast<size_t>(d->max_grid) * 16);
   d->ml = up256(rows * 8);
@@ -275,6 +276,11 @@ sage_status_t sage_fp4_attn_decode(const sage_fp4_cache_t* cache, const sage_fp4
   const float scale = sm_scale > 0.0f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(cache->D));
   p.scale_log2 = scale * 1.4426950408889634f;
   p.c = view_of(*cache, *batch);
+  const int unit = cache->format == SAGE_CACHE_FP4 ? 32 : 8;  // elements in 16 bytes
+  for (int i = 0; i < 3; ++i) {
+    p.ku[i] = static_cast<uint32_t>(cache->k_stride[i] / unit);
+    p.vu[i] = static_cast<uint32_t>(cache->v_stride[i] / unit);
+  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.rec = reinterpret_cast<int4*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + d.rec);

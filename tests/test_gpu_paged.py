@@ -171,7 +171,8 @@ def put(x, page, slot, layout, rows):
 def decode64(q, k, v, sm):
     """One sequence: q [Hq, D], k, v [n, Hkv, D] -> out [Hq, D] and its tolerance, all binary64.
 
-    Weights w~ = w (1 + d): |d| <= u_p (their rounding to the operand type) + e (error of the exponent: the
+    Weights w~ = w (1 + d): |d| <= u_p (their rounding: U[fp16] on FP4 caches; on 16-bit ones a second operand holds
+    what the first rounding left, U^2) + e (error of the exponent: the
     score's binary32 sums, D steps and the scaling, relative to the sum of magnitudes, and the exp2
     approximation's 2^-22, plus the magnitude of the exponent itself times 2^-23). Normalised by their
     own sum, the result is off by at most 2 max|d| sum w |v|; the binary32 accumulation over n / 16 steps per
@@ -191,7 +192,7 @@ def decode64(q, k, v, sm):
 
 def check_decode(case, q, out, sm=None):
     sm = sm or case.D ** -0.5
-    up = U[HF] if case.fmt == "fp4" else U[case.dtype]
+    up = U[HF] if case.fmt == "fp4" else U[case.dtype] ** 2
     u = U[case.dtype]
     worst = 0.0
     for b, n in enumerate(case.lens):

@@ -154,11 +154,12 @@ def test_empty_problems_launch_nothing(sage):
 def test_decode_workspace(sage):
     L = sage.lib()
     size = lambda Hq=8, cache=None, **kw: L.sage_fp4_decode_workspace_bytes(cache or make_cache(sage), make_batch(sage, **kw), Hq)  # noqa: E731
-    # 3 sequences x 2 heads of one 64-key tile: at most 6 shares, two partials of 8 heads each
-    rows = 6 * 2 * 8
+    # 3 sequences x 2 heads of one 64-key tile, each pair counted as one tile more: at most 12 shares,
+    # two partials of 8 heads each
+    rows = 12 * 2 * 8
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
-    assert size() == up(6 * 16) + up(rows * 8) + rows * 128 * 4
-    assert size(Hq=32) == up(6 * 16) + up(2 * rows * 8) + 2 * rows * 128 * 4  # 16 heads a group
+    assert size() == up(12 * 16) + up(rows * 8) + rows * 128 * 4
+    assert size(Hq=32) == up(12 * 16) + up(2 * rows * 8) + 2 * rows * 128 * 4  # 16 heads a group
     assert size(Hq=0) == 0 and size(B=0) == 0 and size(Hq=7) == 0
     # bounded by the number of shares the kernel ever uses
     assert size(B=4096, table_width=4096, table_stride=4096) == size(B=8192, table_width=8192, table_stride=8192)
