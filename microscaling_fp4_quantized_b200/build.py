@@ -9,6 +9,9 @@ of the quantization and attention kernels is tested before the access; a failure
 reported in the device error word and the access skipped).
 
     python -m microscaling_fp4_quantized_b200.build [--force] [--verbose] [--checks]
+
+``csrc/binding.cpp``, the native Python binding of the paged cache operators, becomes the extension
+module ``_binding.so`` next to it (g++, torch's headers and libraries; no CUDA code of its own).
 """
 from __future__ import annotations
 
@@ -18,6 +21,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +30,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsage_fp4.so")
 LIB_CHECKS = os.path.join(PKG, "libsage_fp4_checks.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -59,6 +64,7 @@ def up_to_date(lib: str = LIB) -> bool:
 
 def build(force: bool = False, verbose: bool = False, checks: bool = False) -> str:
     lib = LIB_CHECKS if checks else LIB
+    build_binding(force)
     if not force and up_to_date(lib):
         return lib
     bdir = BUILD + ("_checks" if checks else "")
@@ -89,6 +95,30 @@ def build(force: bool = False, verbose: bool = False, checks: bool = False) -> s
         raise RuntimeError("link failed")
     os.replace(tmp, lib)
     return lib
+
+
+def build_binding(force: bool = False) -> str:
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = (src, os.path.join(INCLUDE, "sage_fp4.h"), os.path.abspath(__file__))
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in deps):
+        return BINDING
+    import torch
+    troot = os.path.dirname(os.path.abspath(torch.__file__))
+    tlib = os.path.join(troot, "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(troot, "include"),
+           "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L", tlib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + tlib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("the binding did not build")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

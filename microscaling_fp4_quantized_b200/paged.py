@@ -2,8 +2,9 @@
 
 The entry points wrap the calls of the same names in ``include/sage_fp4.h``. As in the rest of the package
 they check arguments, allocate outputs and workspace with torch and launch on the current
-stream of the tensors' device; what the device tables hold (lengths, pages, positions) is checked on
-the device and reported by ``device_error()``.
+stream of the tensors' device (natively, in ``csrc/binding.cpp``: a step's kernels take a few microseconds);
+what the device tables hold (lengths, pages, positions) is checked on the device and reported by
+``device_error()``.
 
     cache = sage.PagedKVCache.empty(num_pages, 64, num_kv_heads, head_dim, format="fp4")
     rope = sage.rope_table(max_positions, head_dim)
@@ -15,7 +16,6 @@ the device and reported by ``device_error()``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -24,7 +24,6 @@ import torch
 import microscaling_fp4_quantized_b200 as _sage
 
 CACHE_FORMAT = {"16bit": 0, "fp4": 1}
-_NULL = contextlib.nullcontext()
 
 
 class _Rope(ctypes.Structure):
@@ -50,12 +49,14 @@ class _Batch(ctypes.Structure):
                 ("table_width", ctypes.c_int), ("seq_lens", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p)]
 
 
-_Stride2 = ctypes.c_int64 * 2
 _Stride3 = ctypes.c_int64 * 3
 
 
+_native = None
+
+
 def bind(L) -> None:
-    """Argument types of the paged entry points."""
+    """Argument types of the paged entry points, and their addresses for the native binding."""
     i, vp, sz, f = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
     rows, rope, cache, batch = (ctypes.POINTER(t) for t in (_Rows, _Rope, _Cache, _Batch))
     st = ctypes.POINTER(ctypes.c_int64)
@@ -65,69 +66,28 @@ def bind(L) -> None:
     L.sage_fp4_decode_workspace_bytes.argtypes = [cache, batch, i]
     L.sage_fp4_decode_workspace_bytes.restype = sz
     L.sage_fp4_attn_decode.argtypes = [cache, batch, vp, st, vp, st, i, f, vp, sz, vp]
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("the native binding is missing; build it with "
+                           "`python -m microscaling_fp4_quantized_b200.build`") from e
+    calls = (L.sage_fp4_norm_rope, L.sage_fp4_cache_append, L.sage_fp4_cache_gather,
+             L.sage_fp4_decode_workspace_bytes, L.sage_fp4_attn_decode)
+    _binding.bind(*(ctypes.cast(c, vp).value for c in calls), _sage._check)
+    global _native
+    _native = _binding
 
 
-def _on(device: torch.device):
-    """Makes `device` the current one for a launch."""
-    return _NULL if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _n():
+    """The native binding, with the library loaded."""
+    if _native is None:
+        _sage.lib()
+    return _native
 
 
 def _stride(t: torch.Tensor, d: int) -> int:
     """A dimension of size 1 has no stride that could matter."""
     return t.stride(d) if t.shape[d] != 1 else 0
-
-
-def _check_rows(name: str, t: torch.Tensor, dim: int, dtype: torch.dtype, device: torch.device) -> None:
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    if t.shape[-1] != 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the channel (last) dimension must be contiguous")
-
-
-def _check_table(name: str, t: torch.Tensor, shape: tuple, device: torch.device) -> None:
-    if not t.is_cuda or t.device != device or t.dtype != torch.int32:
-        raise ValueError(f"{name} must be an int32 CUDA tensor on {device}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {list(shape)}")
-
-
-def _rope(D: int, dtype: torch.dtype, device: torch.device, q_weight, k_weight, eps: float, rope,
-          interleaved: bool) -> Optional[_Rope]:
-    if q_weight is None and k_weight is None and rope is None:
-        return None
-    r = _Rope()
-    wdt = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if not w.is_cuda or w.device != device or tuple(w.shape) != (D,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [{D}] CUDA tensor on {device}")
-        if w.dtype not in (dtype, torch.float32) or wdt not in (None, w.dtype):
-            raise ValueError(f"norm weights must both be {dtype} or both float32")
-        wdt = w.dtype
-        setattr(r, name, w.data_ptr())
-    r.weight_f32 = int(wdt == torch.float32)
-    r.eps = float(eps)
-    if rope is not None:
-        if not rope.is_cuda or rope.device != device or rope.dtype != torch.float32 or rope.dim() != 2:
-            raise ValueError(f"rope must be a float32 CUDA tensor [positions, rotary_dim] on {device}")
-        if not rope.is_contiguous():
-            raise ValueError("rope must be contiguous")
-        # A table of no positions has no address; any non-null one says that there is a table.
-        r.rope = rope.data_ptr() or 16
-        r.rope_len, r.rotary_dim = rope.shape
-    r.interleaved = int(bool(interleaved))
-    return r
-
-
-def _rows(x: torch.Tensor, y: torch.Tensor, heads: int, dims: tuple) -> _Rows:
-    sx = _Stride3(*(_stride(x, d) if d >= 0 else 0 for d in dims))
-    sy = _Stride3(*(_stride(y, d) if d >= 0 else 0 for d in dims))
-    return _Rows(x.data_ptr(), y.data_ptr(), heads, sx, sy)
 
 
 def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -155,42 +115,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, q_weight:
     rows, [tokens]; without it token n of a 4-d tensor is at position n. A position outside the table
     is reported by device_error() and its rows are not written. q_out / k_out may be q / k (in place) and
     must not overlap them otherwise. Returns (q_out, k_out)."""
-    if q.dim() == 3:
-        dims, shape = (-1, 1, 0), (q.shape[0],)
-        if rope is not None and positions is None:
-            raise ValueError("packed rows need positions")
-    elif q.dim() == 4 and tensor_layout in ("HND", "NHD"):
-        dims = (0, 1, 2) if tensor_layout == "HND" else (0, 2, 1)
-        shape = (q.shape[0], q.shape[dims[2]])
-    else:
-        raise ValueError("q must be [B, H, N, D] ('HND'), [B, N, H, D] ('NHD') or [tokens, H, D]")
-    D, dev, dtype = q.shape[-1], q.device, q.dtype
-    code = _sage._dtype_code(dtype)
-    _check_rows("q", q, q.dim(), dtype, dev)
-    if k is not None:
-        _check_rows("k", k, q.dim(), dtype, dev)
-        if k.shape[-1] != D or tuple(k.shape[d] for d in (dims[0], dims[2]) if d >= 0) != shape:
-            raise ValueError("q and k disagree on batch, tokens or head dimension")
-    elif k_out is not None or k_weight is not None:
-        raise ValueError("k_out and k_weight need k")
-    if positions is not None:
-        _check_table("positions", positions, shape, dev)
-    r = _rope(D, dtype, dev, q_weight, k_weight, eps, rope, interleaved)
-    outs = []
-    for name, x, y in (("q_out", q, q_out), ("k_out", k, k_out)):
-        if x is not None and y is not None:
-            _check_rows(name, y, q.dim(), dtype, dev)
-            if y.shape != x.shape:
-                raise ValueError(f"{name} must have the shape of its input")
-        outs.append(torch.empty(x.shape, dtype=dtype, device=dev) if x is not None and y is None else y)
-    q_out, k_out = outs
-    B, N = (1,) + shape if len(shape) == 1 else shape
-    qr = _rows(q, q_out, q.shape[dims[1]], dims)
-    kr = _rows(k, k_out, k.shape[dims[1]], dims) if k is not None else None
-    with _on(dev):
-        _sage._check(_sage.lib().sage_fp4_norm_rope(qr, kr, B, N, D, code, r, _sage._ptr(positions), _sage._stream(dev)),
-                     "sage_fp4_norm_rope")
-    return q_out, k_out
+    return _n().norm_rope(q, k, q_weight, k_weight, eps, rope, positions, interleaved, tensor_layout, q_out, k_out)
 
 
 class PagedKVCache:
@@ -212,7 +137,10 @@ class PagedKVCache:
         if not fp4 and (k_sf is not None or v_sf is not None or dtype not in (None, k.dtype)):
             raise ValueError("a 16-bit cache has no scales, and its own dtype")
         for name, t in (("k", k), ("v", v)) + ((("k_sf", k_sf), ("v_sf", v_sf)) if fp4 else ()):
-            _check_rows(name, t, 4, k.dtype, k.device)
+            if not t.is_cuda or t.device != k.device or t.dtype != k.dtype:
+                raise ValueError(f"{name} must be a {k.dtype} CUDA tensor on {k.device}")
+            if t.dim() != 4 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+                raise ValueError(f"{name} must have 4 dimensions with contiguous channels")
         if k.shape != v.shape:
             raise ValueError("k and v must have the same shape")
         dims = (0, 1, 2) if tensor_layout == "HND" else (0, 2, 1)
@@ -235,6 +163,7 @@ class PagedKVCache:
         self._c = _Cache(k.data_ptr(), v.data_ptr(), k_sf.data_ptr() if fp4 else None, v_sf.data_ptr() if fp4 else None,
                          ks, vs, self.num_pages, self.page_size, self.num_kv_heads, D, _sage._dtype_code(self.dtype),
                          CACHE_FORMAT[self.format])
+        self._h = _n().make_cache(ctypes.addressof(self._c), k.device.index)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
@@ -249,24 +178,6 @@ class PagedKVCache:
         k, v = (torch.empty(rows + (head_dim // 2,), dtype=torch.uint8, device=device) for _ in range(2))
         ks, vs = (torch.empty(rows + (head_dim // 16,), dtype=torch.uint8, device=device) for _ in range(2))
         return cls(k, v, ks, vs, dtype=dtype, tensor_layout=tensor_layout)
-
-    def _batch(self, page_table: torch.Tensor, seq_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor]) -> _Batch:
-        dev = self.device
-        if not page_table.is_cuda or page_table.device != dev or page_table.dtype != torch.int32:
-            raise ValueError(f"page_table must be an int32 CUDA tensor on {dev}")
-        if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-            raise ValueError("page_table must be [sequences, pages] with contiguous rows")
-        B, width = page_table.shape
-        _check_table("seq_lens", seq_lens, (B,), dev)
-        if cu_seqlens is not None:
-            _check_table("cu_seqlens", cu_seqlens, (B + 1,), dev)
-        return _Batch(B, page_table.data_ptr(), _stride(page_table, 0), width, seq_lens.data_ptr(),
-                      cu_seqlens.data_ptr() if cu_seqlens is not None else None)
-
-    def _dense(self, name: str, t: torch.Tensor, total: Optional[int]) -> None:
-        _check_rows(name, t, 3, self.dtype, self.device)
-        if tuple(t.shape[1:]) != (self.num_kv_heads, self.head_dim) or total not in (None, t.shape[0]):
-            raise ValueError(f"{name} must be [tokens, {self.num_kv_heads}, {self.head_dim}]")
 
 
 def cache_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
@@ -283,32 +194,7 @@ def cache_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, page_tab
     too, into q_out (may be q), which is returned. Two tokens of a call must not share a slot. A page
     outside the cache, a negative position and one beyond the rotation table are reported by
     device_error(); such a token is left out."""
-    batch = cache._batch(page_table, seq_lens, cu_seqlens)
-    cache._dense("k", k, None)
-    total, dev, D = k.shape[0], cache.device, cache.head_dim
-    cache._dense("v", v, total)
-    if cu_seqlens is None and total != batch.B:
-        raise ValueError("without cu_seqlens, k and v hold one token per sequence")
-    r = _rope(D, cache.dtype, dev, q_weight, k_weight, eps, rope, interleaved)
-    rows = None
-    if q is not None:
-        _check_rows("q", q, 3, cache.dtype, dev)
-        if q.shape[0] != total or q.shape[2] != D:
-            raise ValueError(f"q must be [{total}, heads, {D}]")
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            _check_rows("q_out", q_out, 3, cache.dtype, dev)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have the shape of q")
-        rows = _rows(q, q_out, q.shape[1], (-1, 1, 0))
-    elif q_out is not None or q_weight is not None:
-        raise ValueError("q_out and q_weight need q")
-    ks, vs = (_Stride2(_stride(t, 1), _stride(t, 0)) for t in (k, v))
-    with _on(dev):
-        _sage._check(_sage.lib().sage_fp4_cache_append(cache._c, batch, k.data_ptr(), ks, v.data_ptr(), vs, total, r, rows,
-                                                       _sage._stream(dev)), "sage_fp4_cache_append")
-    return q_out
+    return _n().append(cache._h, k, v, page_table, seq_lens, cu_seqlens, q, q_weight, k_weight, eps, rope, interleaved, q_out)
 
 
 def cache_gather(cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, *,
@@ -319,32 +205,12 @@ def cache_gather(cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.
     [total, Hkv, D] (without cu_seqlens: of the last one). total counts the rows; it is needed with
     cu_seqlens unless k_out and v_out are given, and may be larger than cu_seqlens[B]. Rows without a
     token are not written. FP4 values are decoded exactly. Returns (k_out, v_out)."""
-    batch = cache._batch(page_table, seq_lens, cu_seqlens)
-    if (k_out is None) != (v_out is None):
-        raise ValueError("pass both of k_out and v_out, or neither")
-    if total is None:
-        if k_out is None and cu_seqlens is not None:
-            raise ValueError("cu_seqlens needs total, the number of rows")
-        total = k_out.shape[0] if k_out is not None else batch.B
-    if total < 0 or (cu_seqlens is None and total != batch.B):
-        raise ValueError("without cu_seqlens there is one row per sequence")
-    if k_out is None:
-        shape = (total, cache.num_kv_heads, cache.head_dim)
-        k_out, v_out = (torch.empty(shape, dtype=cache.dtype, device=cache.device) for _ in range(2))
-    else:
-        cache._dense("k_out", k_out, total)
-        cache._dense("v_out", v_out, total)
-    ks, vs = (_Stride2(_stride(t, 1), _stride(t, 0)) for t in (k_out, v_out))
-    with _on(cache.device):
-        _sage._check(_sage.lib().sage_fp4_cache_gather(cache._c, batch, k_out.data_ptr(), ks, v_out.data_ptr(), vs, total,
-                                                       _sage._stream(cache.device)), "sage_fp4_cache_gather")
-    return k_out, v_out
+    return _n().gather(cache._h, page_table, seq_lens, cu_seqlens, total, k_out, v_out)
 
 
 def decode_workspace_bytes(cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, num_q_heads: int) -> int:
     """Workspace of sageattn_decode for these shapes."""
-    batch = cache._batch(page_table, seq_lens, None)
-    return int(_sage.lib().sage_fp4_decode_workspace_bytes(cache._c, batch, num_q_heads))
+    return _n().workspace(cache._h, page_table, seq_lens, num_q_heads)
 
 
 def sageattn_decode(q: torch.Tensor, cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, *,
@@ -356,28 +222,7 @@ def sageattn_decode(q: torch.Tensor, cache: PagedKVCache, page_table: torch.Tens
     as zeros, both reported by device_error(). workspace: uint8, 256-byte aligned, of at least
     decode_workspace_bytes(); one that calls share must not serve two at once (allocated per call
     when left out)."""
-    batch = cache._batch(page_table, seq_lens, None)
-    dev, Hq = cache.device, q.shape[1] if q.dim() == 3 else 0
-    for name, t in (("q", q),) if out is None else (("q", q), ("out", out)):
-        _check_rows(name, t, 3, cache.dtype, dev)
-        if tuple(t.shape) != (batch.B, Hq, cache.head_dim):
-            raise ValueError(f"{name} must be [{batch.B}, heads, {cache.head_dim}]")
-    if Hq % cache.num_kv_heads != 0:
-        raise ValueError("the number of query heads must be a multiple of the cache's heads")
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    L = _sage.lib()
-    need = L.sage_fp4_decode_workspace_bytes(cache._c, batch, Hq)
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 CUDA tensor on {dev}")
-    qs, os_ = (_Stride2(_stride(t, 0), _stride(t, 1)) for t in (q, out))
-    with _on(dev):
-        _sage._check(L.sage_fp4_attn_decode(cache._c, batch, q.data_ptr(), qs, out.data_ptr(), os_, Hq, float(sm_scale or 0.0),
-                                            workspace.data_ptr(), workspace.numel(), _sage._stream(dev)),
-                     "sage_fp4_attn_decode")
-    return out
+    return _n().decode(cache._h, q, page_table, seq_lens, sm_scale, out, workspace)
 
 
 def sageattn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, page_table: torch.Tensor,
@@ -400,6 +245,6 @@ def sageattn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: P
     q = cache_append(cache, k, v, page_table, seq_lens, cu_seqlens=cu_seqlens, q=q, q_weight=q_weight, k_weight=k_weight,
                      eps=eps, rope=rope, interleaved=interleaved)
     k, v = cache_gather(cache, page_table, seq_lens, cu_seqlens=cu_seqlens_kv, total=total_kv)
-    with _on(cache.device):
+    with torch.cuda.device(cache.device):
         return _sage.sageattn_varlen(q, k, v, cu_seqlens, cu_seqlens_kv, max_seqlen, max_seqlen_kv, is_causal=is_causal,
                                      **attn)

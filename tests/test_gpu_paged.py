@@ -728,8 +728,7 @@ def test_refusals_on_the_gpu(sage):
     with pytest.raises(sage.SageError):
         sage.cache_append(cache, k.transpose(0, 1).contiguous().view(-1)[4:4 + 2 * 128].view(1, 2, 128), k[:1], table[:1], lens[:1])
     with pytest.raises(sage.SageError) as e:
-        sage.PagedKVCache.empty(2, 16, 2, 96)._dense  # building it is fine; using it is refused
-        c96 = sage.PagedKVCache.empty(2, 16, 2, 96)
+        c96 = sage.PagedKVCache.empty(2, 16, 2, 96)  # building it is fine; using it is refused
         z = torch.zeros(2, 2, 96, dtype=BF, device="cuda")
         sage.cache_append(c96, z, z, table, lens)
     assert e.value.status == sage.SAGE_ERR_UNSUPPORTED
