@@ -12,6 +12,8 @@
 // that neither ragged lengths nor few pairs leave SMs idle. A CTA finishes the pairs that lie
 // inside its share and leaves the (at most two) that cross its borders as partial (max, sum, output)
 // triples; join_kernel adds those up in the order of the shares, so results do not depend on timing.
+// Small problems (see launch_one) take a cluster of up to 8 CTAs per pair instead, which joins its parts
+// through distributed shared memory, in one launch.
 //
 // Each of the four warps owns 16 or 32 keys of a tile and its own ring of cp.async stages, so
 // the main loop has no block barrier; the warps meet when a pair ends. Scores are formed transposed,
@@ -20,12 +22,12 @@
 // the operand of O^T = V^T P^T. The running maximum is raised only when a score exceeds it by
 // 2^4, checked by one vote per tile: probabilities then reach 2^4 times the scale they are kept at.
 //
-// Measured on one B200 with its join, share of the 6549 GB/s a copy reaches: 16-bit, 16 sequences of 256 to
-// 16384 tokens, 32 heads on 8, D 128: 98.8 us, 5.11 TB/s (0.78; torch's sum over as many contiguous bytes reads
-// 5.84 TB/s). 16-bit, 8 sequences of 2000 to 8192, 16 heads, D 64: 39.8 us, 4.2 TB/s (0.64). FP4, 64 sequences of 128 to
-// 8192, 32 heads on 8: 84.6 us, 3.86 TB/s (0.59); one sequence of 131071: 44.7 us, 3.4 TB/s (0.52). FP4 is bound by
-// the instructions that decode it, about 350 per 16 keys at 2.4 a cycle and SM (one conversion and one
-// scaling per two elements are 128 of them); the join costs 2 to 4 us of each.
+// Measured on one B200, joins included, share of the 6549 GB/s a copy reaches: 16-bit, 16 sequences of 256 to 16384
+// tokens, 32 heads on 8, D 128: 82.7 us, 6.11 TB/s (0.93). 16-bit, 8 sequences of 2000 to 8192, 16 heads, D 64: 33.1 us, 5.06
+// TB/s (0.77). FP4, 64 sequences of 128 to 8192, 32 heads on 8: 81 us, 4.03 TB/s (0.62); one sequence of 131071:
+// 42.6 us, 3.54 TB/s (0.54). FP4 is bound by the instructions that decode it, about 350 per 16 keys at 2.4 a
+// cycle and SM (one conversion and one scaling per two elements are 128 of them); a second launch, the
+// join, costs 2 to 4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -41,6 +43,7 @@ namespace sage {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kMaxCluster = 8;  // the portable size
 constexpr int kThreads = 32 * kWarps;
 // Probabilities are kept as 2^kShift exp2(s - m): fp16 then keeps 11 bits for weights down to 2^-22
 // of the maximum, and the largest (2^kShift 2^4) is far from its limit. The factor cancels in the end.
@@ -114,6 +117,27 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of CTA `rank` of the cluster, at the place of this CTA's `p`.
+__device__ __forceinline__ uint32_t at_rank(const void* p, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_cluster2(const float* p, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at_rank(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(const float* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at_rank(p, rank)) : "memory");
+  return v;
+}
+
 // Weights of two heads rounded into one operand word; a and b become the rounded values.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack_p(float& a, float& b) {
@@ -141,10 +165,10 @@ struct Smem {
   static constexpr int kV = kKeys * kKey;                                 // offsets in a stage
   [[maybe_unused]] static constexpr int kKs = 2 * kV, kVs = kKs + kKeys * kSf;
   static constexpr int kStage = 2 * kKeys * (kKey + kSf);
-  // Measured (us): 16-bit D = 128, 16 sequences of 256 to 16384 tokens, 8 heads: 3 stages of 16 keys and two CTAs an
-  // SM 98.8, 2 stages and three CTAs 100.9. D = 64, 8 sequences of 2000 to 8192, 16 heads: 2 stages of 32 keys and
-  // three CTAs 39.8, 3 and two 40.9. FP4, 64 sequences of 128 to 8192: 2 stages and four CTAs 91, 3 and
-  // three 97, 4 and two 112; 16 keys a warp and tile 106.
+  // Measured when chosen (us): 16-bit D = 128, 16 sequences of 256 to 16384 tokens, 8 heads: 3 stages of 16 keys and two
+  // CTAs an SM 98.8, 2 stages and three CTAs 100.9. D = 64, 8 sequences of 2000 to 8192, 16 heads: 2 stages of 32
+  // keys and three CTAs 39.8, 3 and two 40.9. FP4, 64 sequences of 128 to 8192: 2 stages and four CTAs 91, 3
+  // and three 97, 4 and two 112; 16 keys a warp and tile 106.
   static constexpr int kStages = !FP4 && D == 128 ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kMeet = kWarps * 4 * D * 4;  // four heads at a time
@@ -348,71 +372,91 @@ struct Cursor {
 
 }  // namespace
 
-template <typename T, int D, int NT, bool FP4>
-__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2 : 3) decode_kernel(const DecodeParams p) {
+// DIRECT: a cluster of p.cluster CTAs takes one pair, each an equal part of its tiles, and joins the parts through
+// distributed shared memory: no partials in global memory, no second launch.
+template <typename T, int D, int NT, bool FP4, bool DIRECT>
+__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2 : 3)
+    decode_kernel(const __grid_constant__ DecodeParams p) {
   using S = Smem<D, FP4>;
   constexpr bool kMmaBf16 = Is<T>::bf16 && !FP4;  // FP4 values are exact in fp16
   constexpr int KS = D / 16;                      // contraction steps of S^T, channel tiles of O^T
   constexpr int KW = S::kKeys, G = KW / 16;       // keys of a warp and tile, in groups of 16
-  extern __shared__ __align__(16) uint8_t smem[];
+  // All shared memory is this array: behind any static one it would begin off a 128-byte line, and the copies into
+  // it then take two requests each (measured: 108 us instead of 82 for 16 sequences of 8192 tokens, 8 heads).
+  extern __shared__ __align__(1024) uint8_t smem[];
   float* meet = reinterpret_cast<float*>(smem + S::kRing);
   float* meet_ml = meet + kWarps * 4 * D;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, t4 = lane & 3;
   const CacheView& c = p.c;
   const int HC = c.Hkv * p.chunks;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // join_kernel may be launched: it waits for the end
-
-  // This CTA's share, and where it begins.
-  int64_t before;
-  __shared__ int64_t s_red[kWarps];
-  __shared__ int s_b;
-  __shared__ int64_t s_before;
-  const int64_t W = count_tiles<FP4, D>(c, s_red, &before, blockIdx.x == 0 ? p.err : nullptr) * HC;
-  const int64_t u0 = share(W, blockIdx.x, p.grid), u1 = share(W, blockIdx.x + 1, p.grid);
-  {
-    const int per = (c.B + kThreads - 1) / kThreads;
-    const int lo = min(c.B, tid * per), hi = min(c.B, lo + per);
-    for (int b = lo; b < hi; ++b) {
-      const int64_t n = tiles_of<FP4, D>(length_of(c, b, nullptr)) + kPairCost;
-      if (before * HC <= u0 && u0 < (before + n) * HC) {
-        s_b = b;
-        s_before = before;
-      }
-      before += n;
-    }
-  }
-  __syncthreads();
-  const bool by_pair = p.joins < p.grid;  // (see the records below)
-  const int span = static_cast<int>(u1 - u0);
   Cursor pc;  // where the copies are
   pc.at = 0;
-  if (span > 0) {
-    pc.b = s_b;
-    pc.len = length_of(c, pc.b, nullptr);
-    pc.nt = tiles_of<FP4, D>(pc.len);
-    const int64_t in = u0 - s_before * HC;
-    const int hc = static_cast<int>(in / (pc.nt + kPairCost));
-    const int rest = static_cast<int>(in - static_cast<int64_t>(hc) * (pc.nt + kPairCost)) - kPairCost;
-    pc.t = max(rest, 0);
-    pc.at = max(-rest, 0);
+  int span;
+  [[maybe_unused]] int64_t u0 = 0, W = 0;
+  [[maybe_unused]] bool by_pair = false;
+  if constexpr (DIRECT) {
+    const int pair = blockIdx.x / p.cluster, rank = blockIdx.x - pair * p.cluster;
+    const int hc = pair % HC;
+    pc.b = pair / HC;
     pc.hk = hc / p.chunks;
     pc.chunk = hc - pc.hk * p.chunks;
-  }
-  if (pc.at >= span) {  // no tile in this share (uniform over the block): a join skips it
-    if (tid < 8 * NT) {
-      float* ml = p.part_ml + (static_cast<int64_t>(blockIdx.x) * 2 * (8 * NT) + tid) * 2;
-      ml[0] = -INFINITY;
-      ml[1] = 0.0f;
+    pc.len = length_of(c, pc.b, hc == 0 && rank == 0 && tid == 0 ? p.err : nullptr);
+    pc.nt = tiles_of<FP4, D>(pc.len);
+    pc.t = static_cast<int>(static_cast<int64_t>(pc.nt) * rank / p.cluster);
+    span = static_cast<int>(static_cast<int64_t>(pc.nt) * (rank + 1) / p.cluster) - pc.t;
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // join_kernel may be launched: it waits for the end
+    // This CTA's share, and where it begins.
+    int64_t before;
+    int64_t* red = reinterpret_cast<int64_t*>(meet);  // (not in use yet): per warp, then where the share begins
+    int64_t& s_before = red[kWarps];
+    int64_t& s_b = red[kWarps + 1];
+    W = count_tiles<FP4, D>(c, red, &before, blockIdx.x == 0 ? p.err : nullptr) * HC;
+    u0 = share(W, blockIdx.x, p.grid);
+    span = static_cast<int>(share(W, blockIdx.x + 1, p.grid) - u0);
+    {
+      const int per = (c.B + kThreads - 1) / kThreads;
+      const int lo = min(c.B, tid * per), hi = min(c.B, lo + per);
+      for (int b = lo; b < hi; ++b) {
+        const int64_t n = tiles_of<FP4, D>(length_of(c, b, nullptr)) + kPairCost;
+        if (before * HC <= u0 && u0 < (before + n) * HC) {
+          s_b = b;
+          s_before = before;
+        }
+        before += n;
+      }
     }
-    if (tid == 0 && !by_pair) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
+    __syncthreads();
+    by_pair = p.joins < p.grid;  // (see the records below)
+    if (span > 0) {
+      pc.b = static_cast<int>(s_b);
+      pc.len = length_of(c, pc.b, nullptr);
+      pc.nt = tiles_of<FP4, D>(pc.len);
+      const int64_t in = u0 - s_before * HC;
+      const int hc = static_cast<int>(in / (pc.nt + kPairCost));
+      const int rest = static_cast<int>(in - static_cast<int64_t>(hc) * (pc.nt + kPairCost)) - kPairCost;
+      pc.t = max(rest, 0);
+      pc.at = max(-rest, 0);
+      pc.hk = hc / p.chunks;
+      pc.chunk = hc - pc.hk * p.chunks;
+    }
+    if (pc.at >= span) {  // no tile in this share (uniform over the block): a join skips it
+      if (tid < 8 * NT) {
+        float* ml = p.part_ml + (static_cast<int64_t>(blockIdx.x) * 2 * (8 * NT) + tid) * 2;
+        ml[0] = -INFINITY;
+        ml[1] = 0.0f;
+      }
+      if (tid == 0 && !by_pair) p.rec[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      return;
+    }
   }
   Cursor cc = pc;  // where the arithmetic is
 
   auto advance = [&](Cursor& x) {
     ++x.at;
-    if (++x.t < x.nt) return;
+    ++x.t;
+    if (DIRECT || x.t < x.nt) return;
     x.at += kPairCost;
     x.t = 0;
     if (++x.chunk < p.chunks) return;
@@ -477,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
     else copy_rows(page >= 0 ? ko : 0xffffffffu, page >= 0 ? vo : 0xffffffffu, stage, std::false_type{});
   };
 
-  int page = page_of(pc);
+  int page = pc.at < span ? page_of(pc) : -1;
 #pragma unroll
   for (int i = 0; i < S::kStages - 1; ++i) {
     if (pc.at < span) {
@@ -494,7 +538,11 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
   float o[NT][KS][4], m[NT][2], rise[NT][2], shift[NT][2], l[NT][2], qs[NT][2];
   uint32_t slot = 0, fill = S::kStages - 1;  // stages to read and to refill
   bool first = true;
-  int head0 = 0, heads = 0;
+  int head0 = pc.hk * p.group + pc.chunk * p.chunk_heads, heads = min(p.chunk_heads, p.group - pc.chunk * p.chunk_heads);
+  // (DIRECT) the CTA's part for the others: outputs [8 NT][D], then (maximum, sum) per head. It takes
+  // the ring's place, whose last tile has been read when the warps meet.
+  [[maybe_unused]] float* part_o = reinterpret_cast<float*>(smem);
+  [[maybe_unused]] float* part_ml = part_o + 8 * NT * D;
   while (cc.at < span) {
     if (first) {  // a new pair: its queries
       first = false;
@@ -650,13 +698,13 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
 
     const Cursor at = cc;
     advance(cc);
-    if (at.t + 1 < at.nt && cc.at < span) continue;
+    if ((DIRECT || at.t + 1 < at.nt) && cc.at < span) continue;
     // The pair ends, here or with this share: the warps meet.
     first = true;
-    const bool begun = at.at >= at.t, whole = begun && at.t + 1 == at.nt;
+    const bool begun = at.at >= at.t, whole = DIRECT ? p.cluster == 1 : begun && at.t + 1 == at.nt;
     // Partial 0: a pair that began before this share; partial 1: one that only goes on after it.
     const int part = begun ? 1 : 0;
-    if (tid == 0 && (by_pair ? begun : cc.at >= span)) {
+    if (!DIRECT && tid == 0 && (by_pair ? begun : cc.at >= span)) {
       // What join_kernel has to do, one record per pair (by the CTA with the pair's first tile) or, when
       // there are more pairs than CTAs, one per CTA (for the pair that goes on after it).
       int4 rec = make_int4(-1, 0, 0, 0);
@@ -724,6 +772,14 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
           if (whole) {
             T* out = static_cast<T*>(p.out) + at.b * p.sob + static_cast<int64_t>(head0 + n * 8 + h) * p.soh + c0;
             store_out<T, N>(out, acc, sum);
+          } else if constexpr (DIRECT) {
+            float2* po = reinterpret_cast<float2*>(part_o + (n * 8 + h) * D + c0);
+#pragma unroll
+            for (int e = 0; e < N; e += 2) po[e / 2] = make_float2(acc[e], acc[e + 1]);
+            if ((tid & 31) == 0) {
+              part_ml[(n * 8 + h) * 2] = mx;
+              part_ml[(n * 8 + h) * 2 + 1] = sum;
+            }
           } else {
             const int64_t g = (static_cast<int64_t>(blockIdx.x) * 2 + part) * (8 * NT) + n * 8 + h;
             float2* po = reinterpret_cast<float2*>(p.part_o + g * D + c0);
@@ -738,12 +794,47 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
       }
     }
   }
+  if constexpr (DIRECT) {
+    if (p.cluster == 1) return;  // uniform over the grid
+    if (span <= 0 && tid < 8 * NT) part_ml[2 * tid] = -INFINITY;  // no tile here, no output
+    cluster_sync();
+    constexpr int Q = D / 4;  // a thread's piece: 4 channels of a head
+    const int rank = blockIdx.x % p.cluster;
+    for (int i = rank * kThreads + tid; i < heads * Q; i += p.cluster * kThreads) {
+      const int h = i / Q, c0 = (i - h * Q) * 4;
+      float2 ml[kMaxCluster];
+      float4 v[kMaxCluster];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        ml[r].x = -INFINITY;
+        if (r < p.cluster) {
+          ml[r] = ld_cluster2(part_ml + 2 * h, r);
+          if (ml[r].x != -INFINITY) v[r] = ld_cluster4(part_o + h * D + c0, r);
+        }
+        mx = fmaxf(mx, ml[r].x);
+      }
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (ml[r].x == -INFINITY) continue;
+        const float f = ex2_approx(ml[r].x - mx);
+        sum += ml[r].y * f;
+        acc[0] += v[r].x * f;
+        acc[1] += v[r].y * f;
+        acc[2] += v[r].z * f;
+        acc[3] += v[r].w * f;
+      }
+      store_out<T, 4>(static_cast<T*>(p.out) + pc.b * p.sob + static_cast<int64_t>(head0 + h) * p.soh + c0, acc, sum);
+    }
+    cluster_sync();  // the parts stay until every CTA has read them
+  }
 }
 
 // Adds up the partial results of the pairs that lie in more than one share. Block (record, head);
 // 8 groups of 16 threads take every eighth share each, then meet.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(128) join_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int N = D / 16;
   __shared__ float s_acc[8][D];
   __shared__ float s_ml[8][2];
@@ -849,23 +940,45 @@ template <typename T, int D, int NT, bool FP4>
 cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   constexpr int smem = Smem<D, FP4>::kBytes;
   cudaError_t e = cudaSuccess;
-  const int fit = resident_ctas<decode_kernel<T, D, NT, FP4>>(smem, &e);
+  const int fit = resident_ctas<decode_kernel<T, D, NT, FP4, false>>(smem, &e);
   if (e != cudaSuccess) return e;
-  p.grid = max_grid < fit ? max_grid : fit;
   const int64_t pairs = static_cast<int64_t>(p.c.B) * p.c.Hkv * p.chunks;
-  p.joins = static_cast<int>(pairs < p.grid ? pairs : p.grid);
-  decode_kernel<T, D, NT, FP4><<<p.grid, kThreads, smem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.c.capacity <= tile_keys(FP4, D)) return cudaSuccess;  // one tile per pair: none is split
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.joins, p.chunk_heads);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  cfg.stream = stream;
+  const int tiles = p.c.capacity > 0 ? (p.c.capacity - 1) / tile_keys(FP4, D) + 1 : 1;
+  int cluster = 1;
+  while (cluster < kMaxCluster && cluster < tiles && pairs * cluster * 2 <= fit) cluster *= 2;
+  // One launch by pairs where a CTA then has few tiles: at most 8 (lengths may be ragged, and nothing evens them
+  // out), and no more than three above its share of all tiles, which is about what the second launch
+  // costs; with far more pairs than CTAs the shares' pipeline across pairs wins. Measured by pairs / by
+  // shares (us, 32 heads on 8, D 128): 16-bit, 1 x 64 tokens 3.7 / 4.6, 1 x 1024 6.8 / 6.9, 1 x 4096 11.3 / 9.3, 4 x 2048
+  // 9.8 / 10.7, 16 x 512 8.9 / 11.2, 16 x 1024 16.4 / 18.3, 16 x 1024..8192 63 / 48, 64 x 512 27.2 / 29.7, 200 x 64 22.5 / 19.4; FP4,
+  // 1 x 1024 6.7 / 7.8, 16 x 4096 24.3 / 26.8, 64 x 1024 23.0 / 28.7, 64 x 256..2048 35.0 / 32.4, 200 x 512 34.4 / 42.6.
+  const int per = (tiles + cluster - 1) / cluster;
+  if (pairs <= 3 * static_cast<int64_t>(fit) && per <= 8 && per <= pairs * (tiles + 1) / fit + 3) {
+    resident_ctas<decode_kernel<T, D, NT, FP4, true>>(smem, &e);
+    if (e != cudaSuccess) return e;
+    p.cluster = cluster;
+    cfg.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    return cudaLaunchKernelEx(&cfg, decode_kernel<T, D, NT, FP4, true>, p);
+  }
+  p.grid = max_grid < fit ? max_grid : fit;
+  p.joins = static_cast<int>(pairs < p.grid ? pairs : p.grid);
+  decode_kernel<T, D, NT, FP4, false><<<p.grid, kThreads, smem, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.c.capacity <= tile_keys(FP4, D)) return cudaSuccess;  // one tile per pair: none is split
+  cfg.gridDim = dim3(p.joins, p.chunk_heads);
+  cfg.blockDim = dim3(128);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, join_kernel<T, D, NT>, p);
 }
 

@@ -472,6 +472,24 @@ def test_decode(sage, oracle_mod, fmt, dtype, lens, page, Hkv, group, D, layout)
 
 
 @pytest.mark.parametrize("fmt", ["16bit", "fp4"])
+@pytest.mark.parametrize("B,Hkv,width", [(1, 1, 16), (1, 8, 64), (3, 8, 128), (16, 8, 40), (70, 8, 30), (300, 3, 8), (9, 2, 4096)])
+def test_decode_by_pairs_and_by_shares(sage, oracle_mod, fmt, B, Hkv, width):
+    """Tables of widths that take one CTA, a cluster of 2, 4 or 8 per pair, and (the last) shares: the split follows
+    the table, the lengths may be anything in it, down to nothing."""
+    g = torch.Generator().manual_seed(B)
+    top = min(width * 16, 1200)
+    lens = torch.randint(0, top + 1, (B,), generator=g).tolist()
+    lens[0] = top
+    c = Case(sage, lens, 16, Hkv, 64, BF, fmt, width=width).fill(oracle_mod, B)
+    q = randn(gen(B + 1), B, Hkv * 3, 64)
+    out = sage.sageattn_decode(q, c.cache, c.table, c.seq_lens)
+    check_decode(c, q, out)
+    ws = torch.full((sage.decode_workspace_bytes(c.cache, c.table, c.seq_lens, q.shape[1]),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    assert torch.equal(out, sage.sageattn_decode(q, c.cache, c.table, c.seq_lens, workspace=ws))
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "fp4"])
 def test_decode_one_long_sequence(sage, oracle_mod, fmt):
     """More shares than any other case; the last tokens matter as much as the first."""
     c = Case(sage, [70001], 64, 1, 128, BF, fmt).fill(oracle_mod, 21)
