@@ -40,10 +40,17 @@ __device__ __forceinline__ uint32_t block_scale_byte(float a) {
 // E2M1 rounding is symmetric too, so the codes come out with every sign bit inverted,
 // which one XOR puts back. (Checked on the CPU for every E4M3 divisor and every finite
 // quotient tried, +-0 and underflowing products included: tests/div_identity.c.)
+//
+// r = RN(1/s) for a positive E4M3 s: the approximate reciprocal is off by e, |e| <= 2^-23 or so; 1 - s r0 = e is exact
+// in the FMA (s has 4 significant bits), and r0 + r0 e = (1 - e^2) / s is rounded once. 1/s times its power of two is
+// 1, 8/9, 4/5, 8/11, 2/3, 8/13, 4/7 or 8/15, whose binary periods of at most 12 places keep it further than 2^-46
+// from every rounding border, so the result is the correctly rounded one.
 template <int O, int N>
 __device__ __forceinline__ uint32_t encode8_neg(const float (&x)[N], float s) {
   if (s == 0.0f) return 0u;
-  const float nr = -__frcp_rn(s);
+  float r0;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(s));
+  const float nr = -__fmaf_rn(r0, __fmaf_rn(-s, r0, 1.0f), r0);
   const float2 nr2 = make_float2(nr, nr), s2 = make_float2(s, s);
   float y[8];
 #pragma unroll

@@ -133,6 +133,20 @@ __device__ __forceinline__ float rsqrt_exact(double m, float2 (&xa)[4], float2 (
   return static_cast<float>(y * back);
 }
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Largest magnitude of x[O .. O + 7]; NaN if one of them is.
+template <int O>
+__device__ __forceinline__ float absmax8(const float (&x)[16]) {
+  float a = max3_nan(fabsf(x[O]), fabsf(x[O + 1]), fabsf(x[O + 2]));
+  a = max3_nan(a, fabsf(x[O + 3]), fabsf(x[O + 4]));
+  a = max3_nan(a, fabsf(x[O + 5]), fabsf(x[O + 6]));
+  return max3_nan(a, fabsf(x[O + 7]), 0.0f);
+}
+
 // Where a token of an append or gather call lies in the cache.
 struct Place {
   int64_t page;  // -1: nowhere (outside the sequences, or refused and reported)
@@ -187,13 +201,13 @@ __device__ __forceinline__ Place place_of(const CacheView& c, int tok, bool lead
 // Rows in flight per lane group: four loaded together, or two with the next two already on their way
 // where the arithmetic of quantization has to be hidden. Measured (us, 128 registers, 16 warps an
 // SM): norm and interleaved rotation of B1 H24 N32768 D128 143 against 143, prompt of 8191 tokens with 32 + 8
-// heads 31.8 against 35.6, append of 17,995 tokens to an FP4 cache and its read 131 against 115. Three
+// heads 31.8 against 35.6, append of 17,995 tokens to an FP4 cache and its read 131 against 115 (when chosen). Three
 // blocks' worth of registers (80) spill and lose a quarter; 8 channels a lane need as many instructions
 // for half the bytes and lose 40 %.
 template <typename T, int D, bool CACHE, bool FP4, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int LPR = D / 16, GPW = 32 / LPR;
-  constexpr int kUnroll = FP4 ? 2 : 4;
+    constexpr int kUnroll = FP4 ? 2 : 4;
   constexpr bool kAhead = FP4;
   const int lane = threadIdx.x & 31, j = lane % LPR;
   const int items = p.items_q + p.items_k + p.items_v;
@@ -379,12 +393,12 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
       float x[16];  // channels of the two chunks in order
       join<INTER>(xa, xb, x);
       if (FP4 && paged) {
-        float ma = 0.0f, mb = 0.0f;
+        float ma = absmax8<0>(x), mb = absmax8<8>(x);
+        if (!(fmaxf(ma, mb) < INFINITY) || ma != ma || mb != mb) {  // saturate (NaN: to the largest)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[i] = fmaxf(fminf(x[i], FLT_MAX), -FLT_MAX);  // saturate (NaN: to the largest)
-          if (i < 8) ma = fmaxf(ma, fabsf(x[i]));
-          else mb = fmaxf(mb, fabsf(x[i]));
+          for (int i = 0; i < 16; ++i) x[i] = fmaxf(fminf(x[i], FLT_MAX), -FLT_MAX);
+          ma = absmax8<0>(x);
+          mb = absmax8<8>(x);
         }
         // A block is two neighbouring chunks: this lane's two, or one each of lanes j and j ^ 1.
         const float na = __shfl_xor_sync(0xffffffffu, ma, 1), nb = __shfl_xor_sync(0xffffffffu, mb, 1);
@@ -500,11 +514,13 @@ static cudaError_t rows_of_type(const RowsParams& p, int D, bool to_cache, bool 
                        : rows_of<T, 64, false>(p, to_cache, fp4, grid, stream);
 }
 
-// Heads a warp walks: as many as leave four times the warps that are resident (148 SMs of 16), at
-// most 16 (with one time, the prompt above takes 33.0 us instead of 31.8).
-static int heads_of(int64_t groups, int heads) {
+// Heads a warp walks: as many as leave `waves` times the warps that are resident (148 SMs of 16), at
+// most 16. Dense rows: four times (with one, the prompt above takes 32.7 us instead of 31.3). Paged ones: once, as
+// finding a token's place is a chain of loads (with four, keys and values of 17,995 tokens, 8 heads, take 48.4 us
+// instead of 41.5 to FP4 pages and 35.1 instead of 31.8 to 16-bit ones).
+static int heads_of(int64_t groups, int heads, int waves) {
   int n = 16;
-  while (n > 1 && groups * ((heads + n - 1) / n) < 4 * 148 * 16) n /= 2;
+  while (n > 1 && groups * ((heads + n - 1) / n) < waves * 148 * 16) n /= 2;
   return n;
 }
 
@@ -512,7 +528,7 @@ cudaError_t launch_rows(const RowsParams& in, int D, int dtype, bool to_cache, b
   RowsParams p = in;
   const int gpw = 512 / D;
   const int64_t groups = (static_cast<int64_t>(p.T) + gpw - 1) / gpw;
-  const int most = heads_of(groups, p.Hq + p.Hk + p.Hv);
+  const int most = heads_of(groups, p.Hq + p.Hk + p.Hv, to_cache ? 1 : 4);
   auto split = [&](int h, int* items, int* per) {
     *items = (h + most - 1) / most;
     *per = h > 0 ? (h + *items - 1) / *items : 0;
@@ -539,7 +555,7 @@ cudaError_t launch_gather(const GatherParams& in, int D, int dtype, bool fp4, cu
   GatherParams p = in;
   const int gpw = 512 / D;
   const int64_t groups = (static_cast<int64_t>(p.T) + gpw - 1) / gpw;
-  p.heads_per_item = heads_of(groups, 2 * p.c.Hkv);
+  p.heads_per_item = heads_of(groups, 2 * p.c.Hkv, 1);
   p.items = (p.c.Hkv + p.heads_per_item - 1) / p.heads_per_item;
   const int64_t warps = groups * 2 * p.items;
   const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);

@@ -394,6 +394,31 @@ def test_fp4_saturation(sage, oracle_mod):
     assert k[1, 0, 3] == 2688 and k[1, 0, 4] == -2688 and k[1, 0, 5] == 2688 and k[1, 0, 20] == 66 / 64
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_fp4_every_scale_at_every_border(sage, oracle_mod, dtype):
+    """For every scale byte: the block's maximum, values on the borders between codes (ties), one step to either
+    side of them, and their negatives; codes and scales bit for bit."""
+    byte = torch.arange(1, 127, dtype=torch.uint8)
+    s = byte.view(torch.float8_e4m3fn).float()[:, None]
+    ties = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    on = (s * ties).to(dtype)  # at most 7 significant bits: exact
+    step = lambda x, d: (x.view(torch.int16) + d).view(dtype)  # noqa: E731
+    top = (s * 6).to(dtype)
+    rows = []
+    for v in (on, step(on, 1), step(on, -1)):
+        half = torch.cat((v, top), dim=1)
+        rows.append(torch.cat((half, -half), dim=1))
+    x = torch.stack(rows, dim=1).reshape(-1, 16)
+    x = torch.cat((x, x.new_zeros((-len(x)) % 8, 16))).reshape(-1, 1, 128).cuda()
+    c = Case(sage, [len(x)], 16, 1, 128, dtype, "fp4")
+    new = [len(x)]
+    sage.cache_append(c.cache, x, x.flip(0), c.table, c.seq_lens, cu_seqlens=c.cu(new))
+    for rows, codes, sf in ((x, c.k, c.ks), (x.flip(0), c.v, c.vs)):
+        wc, ws = quantized(oracle_mod, rows.float().cpu())
+        np.testing.assert_array_equal(c.at(sf, new).cpu().numpy(), ws)
+        np.testing.assert_array_equal(c.at(codes, new).cpu().numpy(), wc)
+
+
 @pytest.mark.parametrize("fmt", ["16bit", "fp4"])
 def test_bad_tables_are_reported_and_not_followed(sage, oracle_mod, fmt):
     lens = [20, 20, 20, 20]
