@@ -50,7 +50,7 @@ sage_status_t check_cache(const sage_fp4_cache_t* c) {
 
 sage_status_t check_batch(const sage_fp4_cache_t* c, const sage_fp4_batch_t* b, bool rows, int total) {
   if (b == nullptr || b->B < 0 || b->table_width < 0 || b->table_stride < 0 || total < 0) return SAGE_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(b->table_width) * c->page_size >= (int64_t(1) << 31)) return SAGE_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(b->table_width) * c->page_size > (int64_t(1) << 30)) return SAGE_ERR_UNSUPPORTED;
   if (b->B == 0) return SAGE_OK;
   if (!aligned(b->seq_lens, 4) || (b->table_width > 0 && !aligned(b->page_table, 4))) return SAGE_ERR_INVALID_ARG;
   if (rows) {

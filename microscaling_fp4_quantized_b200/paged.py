@@ -56,7 +56,7 @@ _native = None
 
 
 def bind(L) -> None:
-    """Argument types of the paged entry points, and their addresses for the native binding."""
+    """Argument types of the paged entry points."""
     i, vp, sz, f = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
     rows, rope, cache, batch = (ctypes.POINTER(t) for t in (_Rows, _Rope, _Cache, _Batch))
     st = ctypes.POINTER(ctypes.c_int64)
@@ -66,22 +66,22 @@ def bind(L) -> None:
     L.sage_fp4_decode_workspace_bytes.argtypes = [cache, batch, i]
     L.sage_fp4_decode_workspace_bytes.restype = sz
     L.sage_fp4_attn_decode.argtypes = [cache, batch, vp, st, vp, st, i, f, vp, sz, vp]
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise RuntimeError("the native binding is missing; build it with "
-                           "`python -m microscaling_fp4_quantized_b200.build`") from e
-    calls = (L.sage_fp4_norm_rope, L.sage_fp4_cache_append, L.sage_fp4_cache_gather,
-             L.sage_fp4_decode_workspace_bytes, L.sage_fp4_attn_decode)
-    _binding.bind(*(ctypes.cast(c, vp).value for c in calls), _sage._check)
-    global _native
-    _native = _binding
 
 
 def _n():
-    """The native binding, with the library loaded."""
+    """The native binding, with the library's entry points (raises if it is missing)."""
+    global _native
     if _native is None:
-        _sage.lib()
+        L, vp = _sage.lib(), ctypes.c_void_p
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the native binding is missing; build it with "
+                               "`python -m microscaling_fp4_quantized_b200.build`") from e
+        calls = (L.sage_fp4_norm_rope, L.sage_fp4_cache_append, L.sage_fp4_cache_gather,
+                 L.sage_fp4_decode_workspace_bytes, L.sage_fp4_attn_decode)
+        _binding.bind(*(ctypes.cast(c, vp).value for c in calls), _sage._check)
+        _native = _binding
     return _native
 
 
@@ -218,7 +218,7 @@ def sageattn_decode(q: torch.Tensor, cache: PagedKVCache, page_table: torch.Tens
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention of one new token per sequence, q [B, Hq, D], over the seq_lens[b] cached tokens of its sequence
     (its own key and value among them, once appended). Hq is a multiple of the cache's heads. A sequence
-    of length 0 gets zeros; a length outside the page table is clamped and a page outside the cache counts
+    of length 0 gets zeros; out may be q. A length outside the page table is clamped and a page outside the cache counts
     as zeros, both reported by device_error(). workspace: uint8, 256-byte aligned, of at least
     decode_workspace_bytes(); one that calls share must not serve two at once (allocated per call
     when left out)."""

@@ -6,6 +6,10 @@ lanes, its scaling and eps (12 roundings of 2^-24, halved by the root), the reci
 in the last place (4 x 2^-24), then two products, the rotation's product and its sum: 14, bounded by 16;
 attention adds its own terms (decode_tolerance). FP4 codes and scales, copies and reads are exact.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -588,6 +592,73 @@ def test_decode_strided_queries_outputs_and_tables(sage, oracle_mod):
     check_decode(c, q, got)
     assert (out[:, :2] == 7.0).all() and (out[:, 10:] == 7.0).all()
     assert torch.equal(got, sage.sageattn_decode(q, c.cache, c.table, c.seq_lens))
+
+
+def test_decode_in_place(sage, oracle_mod):
+    for lens, width in (([3000, 5, 700], None), ([90, 64], None), ([9000], 1024)):
+        c = Case(sage, lens, 16, 2, 128, BF, "fp4", width=width).fill(oracle_mod, 85)
+        q = randn(gen(86), len(lens), 40, 128)  # 20 heads a group: two chunks
+        want = sage.sageattn_decode(q, c.cache, c.table, c.seq_lens)
+        assert sage.sageattn_decode(q, c.cache, c.table, c.seq_lens, out=q) is q
+        assert torch.equal(q, want)
+
+
+def test_many_sequences(sage, oracle_mod):
+    """More sequences than threads of a block, most of them short or empty; steps for all of them at once."""
+    B = 5000
+    g = torch.Generator().manual_seed(7)
+    lens = torch.where(torch.rand(B, generator=g) < 0.3, 0, torch.randint(0, 40, (B,), generator=g)).tolist()
+    lens = [n + 1 for n in lens]
+    c = Case(sage, lens, 8, 1, 64, HF).fill(oracle_mod, 95)
+    w = torch.randn(64, generator=gen(96), device="cuda")
+    k, v, q = (randn(gen(97 + i), B, 1 + i, 64, dtype=HF) for i in range(3))
+    v, q = v[:, :1], q[:, :2]
+    qr = sage.cache_append(c.cache, k, v, c.table, c.seq_lens, q=q, q_weight=w, k_weight=w, rope=sage.rope_table(64, 64))
+    pos = c.places([1] * B)[2]
+    want, slack = rows64(q, w, sage.rope_table(64, 64), pos, False)
+    assert_rounded(qr, want, slack, HF)
+    kk, vv = sage.cache_gather(c.cache, c.table, c.seq_lens, cu_seqlens=c.cu(lens), total=sum(lens))
+    c.kv64 = list(zip(kk.double().split(lens), vv.double().split(lens)))
+    check_decode(c, qr, sage.sageattn_decode(qr, c.cache, c.table, c.seq_lens))
+
+
+FIRST = """
+import torch, microscaling_fp4_quantized_b200 as sage
+BF = torch.bfloat16
+cache = sage.PagedKVCache.empty(200, 16, 2, 128, dtype=BF, format=%r)
+table = torch.arange(200, dtype=torch.int32, device='cuda').view(2, 100)
+lens = torch.tensor([1600, 900], dtype=torch.int32, device='cuda')
+cu = torch.tensor([0, 1600, 2500], dtype=torch.int32, device='cuda')
+g = torch.Generator('cuda').manual_seed(1)
+k, v = (torch.randn(2500, 2, 128, generator=g, device='cuda').to(BF) for _ in range(2))
+q = torch.randn(2500, 8, 128, generator=g, device='cuda').to(BF)
+rope = sage.rope_table(1600, 128)
+pos = torch.cat((torch.arange(1600), torch.arange(900))).int().cuda()
+
+def step():
+    sage.cache_append(cache, k, v, table, lens, cu_seqlens=cu, rope=rope)
+    qr, kr = sage.qk_norm_rope(q, k, rope=rope, positions=pos)
+    dense = sage.cache_gather(cache, table, lens, cu_seqlens=cu, total=2500)
+    short = sage.sageattn_decode(qr[:2], cache, table[:, :4], lens.clamp(max=64))
+    return qr, kr, *dense, short, sage.sageattn_decode(qr[:2], cache, table, lens)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and sage.device_error() == 0
+print('same')
+"""
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "fp4"])
+def test_first_call_of_a_process_is_captured(sage, fmt):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST % fmt], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
 
 
 def test_shared_prefix_pages(sage, oracle_mod):

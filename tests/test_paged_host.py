@@ -79,7 +79,7 @@ def test_largest_cache_is_accepted(sage):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(B=-1), INV), (dict(table_width=-1), INV), (dict(table_stride=-4), INV), (dict(page_table=None), INV),
-    (dict(page_table=FAKE + 2), INV), (dict(seq_lens=None), INV), (dict(table_width=2 ** 27), UNS),
+    (dict(page_table=FAKE + 2), INV), (dict(seq_lens=None), INV), (dict(table_width=2 ** 26 + 1), UNS),
 ])
 def test_batch_refusals(sage, kw, status):
     b = make_batch(sage, **kw)
