@@ -24,8 +24,8 @@
 //
 // Measured on one B200, joins included, share of the 6549 GB/s a copy reaches: 16-bit, 16 sequences of 256 to 16384
 // tokens, 32 heads on 8, D 128: 82.7 us, 6.11 TB/s (0.93). 16-bit, 8 sequences of 2000 to 8192, 16 heads, D 64: 33.1 us, 5.06
-// TB/s (0.77). FP4, 64 sequences of 128 to 8192, 32 heads on 8: 81 us, 4.03 TB/s (0.62); one sequence of 131071:
-// 42.6 us, 3.54 TB/s (0.54). FP4 is bound by the instructions that decode it, about 350 per 16 keys at 2.4 a
+// TB/s (0.77). FP4, 64 sequences of 128 to 8192, 32 heads on 8: 78.4 us, 4.17 TB/s (0.64); one sequence of 131071:
+// 41.7 us, 3.62 TB/s (0.55). FP4 is bound by the instructions that decode it, about 350 per 16 keys at 2.4 a
 // cycle and SM (one conversion and one scaling per two elements are 128 of them); a second launch, the
 // join, costs 2 to 4 us.
 #include <cuda_bf16.h>
@@ -510,6 +510,24 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
       cp_async_small<S::kSf>(stage + S::kVs + lane * S::kSf, c.v_sf + static_cast<uint64_t>(valid ? vo : 0u) * 2, valid);
     }
   };
+  // The same where the warp's keys lie one behind the other (consecutive slots of one page): one address, at
+  // fixed distances from this lane's own key's, serves all copies of a kind. Measured (us): FP4 batch 81.2 -> 78.4,
+  // one long FP4 sequence 42.7 -> 41.7; 16-bit caches, which are not bound by instructions, the same.
+  auto copy_run = [&](uint32_t ko, uint32_t vo, uint32_t stage) {
+    const int64_t back = static_cast<int64_t>(lane * 16) - (lane % KW) * S::kKey;
+    const char* ks = static_cast<const char*>(c.k) + back + static_cast<uint64_t>(ko) * 16;
+    const char* vs = static_cast<const char*>(c.v) + back + static_cast<uint64_t>(vo) * 16;
+#pragma unroll
+    for (int i = 0; i < KW / KPI; ++i) {
+      const uint32_t flip = FP4 ? 0 : ((KPI * i) & 7) << 4;
+      cp_async16(stage + (k_at ^ flip) + i * KPI * S::kKey, ks + i * 512);
+      cp_async16(stage + S::kV + (v_at ^ flip) + i * KPI * S::kKey, vs + i * 512);
+    }
+    if constexpr (FP4) {
+      cp_async_small<S::kSf>(stage + S::kKs + lane * S::kSf, c.k_sf + static_cast<uint64_t>(ko) * 2, true);
+      cp_async_small<S::kSf>(stage + S::kVs + lane * S::kSf, c.v_sf + static_cast<uint64_t>(vo) * 2, true);
+    }
+  };
   auto copy_tile = [&](const Cursor& x, int page, uint32_t stage) {
     if (x.t * tile_keys(FP4, D) + warp * KW >= x.len) return;
     // This lane's key as row offsets in units of 16 bytes; all ones: no such key.
@@ -517,7 +535,10 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
     const uint32_t slot = pos - div_by_page(c.page, pos) * c.page.d;
     const uint32_t ko = page * p.ku[0] + x.hk * p.ku[1] + slot * p.ku[2];
     const uint32_t vo = page * p.vu[0] + x.hk * p.vu[1] + slot * p.vu[2];
-    if (__all_sync(0xffffffffu, page >= 0)) copy_rows(ko, vo, stage, std::true_type{});
+    if (__all_sync(0xffffffffu, page >= 0)) {
+      if (p.run) copy_run(ko, vo, stage);
+      else copy_rows(ko, vo, stage, std::true_type{});
+    }
     else copy_rows(page >= 0 ? ko : 0xffffffffu, page >= 0 ? vo : 0xffffffffu, stage, std::false_type{});
   };
 
@@ -939,6 +960,7 @@ int resident_ctas(int smem, cudaError_t* e) {
 template <typename T, int D, int NT, bool FP4>
 cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   constexpr int smem = Smem<D, FP4>::kBytes;
+  p.run = p.c.sk.n == D && p.c.sv.n == D && p.c.page.d % Smem<D, FP4>::kKeys == 0;
   cudaError_t e = cudaSuccess;
   const int fit = resident_ctas<decode_kernel<T, D, NT, FP4, false>>(smem, &e);
   if (e != cudaSuccess) return e;

@@ -81,6 +81,7 @@ struct DecodeParams {
   float* part_o;       // [grid, 2, 8 * NT, D]
   float* part_ml;      // [grid, 2, 8 * NT, 2]
   int4* rec;           // [joins] what is to be joined
+  int run;             // a warp's keys are consecutive in memory (set by launch_decode)
   int grid, joins, cluster;  // (set by launch_decode)
   uint32_t* err;
 };
