@@ -1,14 +1,16 @@
 // Row kernels of the paged cache (sm_100a): norm and rotation of query / key heads, the same
 // with keys and values going into cache pages, and reading pages back.
 //
-// One head of one token is a row of D channels. D / 16 lanes own a row, 16 channels each: the two
-// 8-channel chunks a lane owns are the two halves of 8 rotation pairs (i, i + R/2), so neither
-// pairing needs a shuffle; only the mean square and the FP4 block maximum cross lanes. A
-// lane group keeps its token's cosines, sines and norm weights in registers over the heads of its item;
-// the arithmetic runs on two channels per instruction. All three operations are bound by HBM: each
+// One head of one token is a row of D channels. D / 16 lanes own a row, two 8-channel chunks each, as far
+// apart as the two halves of a rotation pair (i, i + R/2): neither pairing needs a shuffle, and
+// neighbouring lanes move neighbouring chunks; only the mean square and the FP4 block maximum cross
+// lanes. A lane group keeps its token's cosines, sines and norm weights in registers over the heads of its
+// item; the arithmetic runs on two channels per instruction. All three operations are bound by HBM: each
 // row is read once and written once. Measured on one B200, share of the 6549 GB/s a copy
-// reaches: norm and rotation of B1 H24 N32768 D128 143 us, 5.75 TB/s (0.88); prompt of 8191 tokens, 32 + 8
-// heads, 31.8 us, 5.33 TB/s (0.81); dense read of 131,481 cached FP4 tokens, 8 heads, 118 us, 5.49 TB/s (0.84).
+// reaches: norm and rotation of B1 H24 N32768 D128 143 us, 5.73 TB/s (0.88); prompt of 8191 tokens, 32 + 8
+// heads, 31.3 us, 5.42 TB/s (0.83); append of 17,995 tokens, 32 query and 8 key/value heads, 92 us, 4.8 TB/s (0.73), to FP4
+// pages 88.5 us, 4.4 TB/s (0.67: the encoding's instructions); dense read of 131,481 cached FP4 tokens, 8 heads, 106 us, 6.08
+// TB/s (0.93).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -255,7 +257,9 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
   const int R = set == 2 || p.rope == nullptr ? 0 : p.R;
   const int half = R / 16;
   const bool rot = j < half;
-  const int ca = rot ? j : R / 8 + 2 * (j - half), cb = rot ? j + half : ca + 1;
+  // The lane's chunks: two as far apart as the halves of the rotated channels, or of the others, so that
+  // neighbouring lanes read and write neighbouring chunks (adjacent pairs per lane fetch every sector twice).
+  const int ca = rot ? j : R / 16 + j, cb = rot ? j + half : ca + D / 16 - half;
 
   // Cosines and sines of the lane's eight pairs, two to a register pair.
   float2 cs[4], sn[4];
@@ -400,23 +404,18 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
           ma = absmax8<0>(x);
           mb = absmax8<8>(x);
         }
-        // A block is two neighbouring chunks: this lane's two, or one each of lanes j and j ^ 1.
-        const float na = __shfl_xor_sync(0xffffffffu, ma, 1), nb = __shfl_xor_sync(0xffffffffu, mb, 1);
-        const uint32_t ba = block_scale_byte(fmaxf(ma, rot ? na : mb)), bb = block_scale_byte(fmaxf(mb, rot ? nb : ma));
+        // A block is two neighbouring chunks, one each of lanes j and j ^ 1.
+        const uint32_t ba = block_scale_byte(fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1)));
+        const uint32_t bb = block_scale_byte(fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1)));
         const uint32_t ea = encode8_neg<0>(x, e4m3_to_f32(ba)), eb = encode8_neg<8>(x, e4m3_to_f32(bb));
         if (ok) {
           char* codes = dst + row / 2;
           uint8_t* scales = sf + row / 16;
-          if (rot) {
-            *reinterpret_cast<uint32_t*>(codes + 4 * ca) = ea;
-            *reinterpret_cast<uint32_t*>(codes + 4 * cb) = eb;
-            if ((j & 1) == 0) {
-              scales[ca / 2] = static_cast<uint8_t>(ba);
-              scales[cb / 2] = static_cast<uint8_t>(bb);
-            }
-          } else {
-            *reinterpret_cast<uint2*>(codes + 4 * ca) = make_uint2(ea, eb);
+          *reinterpret_cast<uint32_t*>(codes + 4 * ca) = ea;
+          *reinterpret_cast<uint32_t*>(codes + 4 * cb) = eb;
+          if ((j & 1) == 0) {
             scales[ca / 2] = static_cast<uint8_t>(ba);
+            scales[cb / 2] = static_cast<uint8_t>(bb);
           }
         }
       } else if (ok) {
@@ -446,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const GatherParams 
   const Strides ss = is_v ? p.c.sv : p.c.sk, ds = is_v ? p.sv : p.sk;
   const char* src = static_cast<const char*>(is_v ? p.c.v : p.c.k);
   const uint8_t* sf = is_v ? p.c.v_sf : p.c.k_sf;
-  char* dst = static_cast<char*>(is_v ? p.v : p.k) + (tok * ds.n + 16 * j) * 2;
+  // The lane's two chunks of 8 channels are D / 2 apart: neighbouring lanes write neighbouring chunks.
+  char* dst = static_cast<char*>(is_v ? p.v : p.k) + (tok * ds.n + 8 * j) * 2;
   const int64_t src_tok = at.page * ss.b + at.slot * ss.n;
   for (int h = h0; h < h1; h += kUnroll) {
     uint4 raw[kUnroll][2];
@@ -454,45 +454,43 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const GatherParams 
     for (int u = 0; u < kUnroll; ++u) {
       if (h + u >= h1) continue;
       const int64_t row = src_tok + static_cast<int64_t>(h + u) * ss.h;
-      if constexpr (FP4) {
-        const uint2 codes = *reinterpret_cast<const uint2*>(src + row / 2 + 8 * j);
-        raw[u][0] = make_uint4(codes.x, codes.y, sf[row / 16 + j], 0);
-      } else {
-        raw[u][0] = ld_stream(src + row * 2 + j * 32);
-        raw[u][1] = ld_stream(src + row * 2 + j * 32 + 16);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (FP4) {
+          raw[u][i].x = *reinterpret_cast<const uint32_t*>(src + row / 2 + 4 * j + i * (D / 4));
+          raw[u][i].y = sf[row / 16 + j / 2 + i * (D / 32)];
+        } else {
+          raw[u][i] = ld_stream(src + row * 2 + 16 * j + i * D);
+        }
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (h + u >= h1) continue;
-      if constexpr (FP4) {
-        // E2M1 times E4M3 has at most six significant bits and fits fp16's range: every product
-        // below is exact, in fp16 and after it in bf16.
-        const float sc = e4m3_to_f32(raw[u][0].z);
-        const __half2 s2 = __floats2half2_rn(sc, sc);
-        uint32_t o[8];
-        const uint32_t wd[2] = {raw[u][0].x, raw[u][0].y};
+      char* row = dst + static_cast<int64_t>(h + u) * ds.h * 2;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t v[4];
-          e2m1x8_to_f16x2(wd[i], v);
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (FP4) {
+          // E2M1 times E4M3 has at most six significant bits and fits fp16's range: every product
+          // below is exact, in fp16 and after it in bf16.
+          const float sc = e4m3_to_f32(raw[u][i].y);
+          const __half2 s2 = __floats2half2_rn(sc, sc);
+          uint32_t v[4], o[4];
+          e2m1x8_to_f16x2(raw[u][i].x, v);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const __half2 m = __hmul2(*reinterpret_cast<const __half2*>(&v[e]), s2);
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
               const float2 f = __half22float2(m);
-              o[4 * i + e] = pack2<T>(f.x, f.y);
+              o[e] = pack2<T>(f.x, f.y);
             } else {
-              o[4 * i + e] = *reinterpret_cast<const uint32_t*>(&m);
+              o[e] = *reinterpret_cast<const uint32_t*>(&m);
             }
           }
+          raw[u][i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        raw[u][0] = make_uint4(o[0], o[1], o[2], o[3]);
-        raw[u][1] = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4*>(row + i * D) = raw[u][i];
       }
-      char* row = dst + static_cast<int64_t>(h + u) * ds.h * 2;
-      *reinterpret_cast<uint4*>(row) = raw[u][0];
-      *reinterpret_cast<uint4*>(row + 16) = raw[u][1];
     }
   }
 }
