@@ -222,7 +222,8 @@ __device__ __forceinline__ void load_q_fp16(const T* q, bool valid, int t4, uint
 // (r, t4) takes channels t4 D/4 .. of keys r and r + 8, one or two whole scale blocks, and
 // step k contracts channels 4k .. 4k+3 of each lane's range.
 template <int D, int NT>
-__device__ __forceinline__ void scores_fp4(const uint8_t* stage, int k0, int r, int t4, const uint32_t (&qf)[NT][D / 16][2], float (&s)[NT][4]) {
+__device__ __forceinline__ void scores_fp4(const uint8_t* stage, int k0, int r, int t4,
+                                           const uint32_t (&qf)[NT][D / 16][2], float (&s)[NT][4]) {
   using S = Smem<D, true>;
   constexpr int W = D / 32;  // code words of a lane and key: 4 or 2
   uint32_t w[2][W], sc[2];
@@ -261,7 +262,8 @@ __device__ __forceinline__ void scores_fp4(const uint8_t* stage, int k0, int r, 
 // the operand wants two keys' values of one channel side by side, so the nibbles of two
 // keys are interleaved before they are decoded.
 template <int D, int NT>
-__device__ __forceinline__ void values_fp4(const uint8_t* stage, int k0, int r, int t4, const uint32_t (&pb)[NT][2], float (&o)[NT][D / 16][4]) {
+__device__ __forceinline__ void values_fp4(const uint8_t* stage, int k0, int r, int t4, const uint32_t (&pb)[NT][2],
+                                           float (&o)[NT][D / 16][4]) {
   using S = Smem<D, true>;
   constexpr int W = D / 64;  // code words of a lane and key: 2 or 1
   uint32_t w[4][W], sc[2];
@@ -390,6 +392,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
   const CacheView& c = p.c;
   const int HC = c.Hkv * p.chunks;
 
+  wait_for_stream();
   Cursor pc;  // where the copies are
   pc.at = 0;
   int span;
@@ -869,7 +872,7 @@ __global__ void __launch_bounds__(16 * kMaxGroups) join_kernel(const __grid_cons
   __shared__ float s_acc[kMaxGroups][D];
   __shared__ float s_ml[kMaxGroups][2];
   const int tid = threadIdx.x, G = blockDim.x >> 4, g = tid >> 4, c0 = (tid & 15) * N, h = blockIdx.y;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_stream();
   const int4 rec = p.rec[blockIdx.x];
   if (rec.x < 0) return;
   const int hk = rec.y / p.chunks, chunk = rec.y - hk * p.chunks;
@@ -972,53 +975,40 @@ cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   const int fit = resident_ctas<decode_kernel<T, D, NT, FP4, false>>(smem, &e);
   if (e != cudaSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(p.c.B) * p.c.Hkv * p.chunks;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.stream = stream;
   const int tiles = p.c.capacity > 0 ? (p.c.capacity - 1) / tile_keys(FP4, D) + 1 : 1;
   int cluster = 1;
   while (cluster < kMaxCluster && cluster < tiles && pairs * cluster * 2 <= fit) cluster *= 2;
-  // One launch by pairs where a CTA then has few tiles: at most 8 (lengths may be ragged, and nothing evens them
-  // out), and no more than three above its share of all tiles, which is about what the second launch
+  // One launch by pairs where a CTA then has few tiles: at most 8 (lengths may be ragged, and nothing evens
+  // them out), and no more than three above its share of all tiles, which is about what the second launch
   // costs; with far more pairs than CTAs the shares' pipeline across pairs wins. Measured by pairs / by
-  // shares (us, 32 heads on 8, D 128): 16-bit, 1 x 64 tokens 3.7 / 4.6, 1 x 1024 6.8 / 6.9, 1 x 4096 11.3 / 9.3, 4 x 2048
-  // 9.8 / 10.7, 16 x 512 8.9 / 11.2, 16 x 1024 16.4 / 18.3, 16 x 1024..8192 63 / 48, 64 x 512 27.2 / 29.7, 200 x 64 22.5 / 19.4; FP4,
-  // 1 x 1024 6.7 / 7.8, 16 x 4096 24.3 / 26.8, 64 x 1024 23.0 / 28.7, 64 x 256..2048 35.0 / 32.4, 200 x 512 34.4 / 42.6.
+  // shares (us, sequences x tokens, 32 heads on 8, D 128): 16-bit, 1 x 64 3.7 / 4.6, 1 x 1024 6.8 / 6.9,
+  // 1 x 4096 11.3 / 9.3, 4 x 2048 9.8 / 10.7, 16 x 512 8.9 / 11.2, 16 x 1024 16.4 / 18.3, 16 x 1024 to 8192
+  // 63 / 48, 64 x 512 27.2 / 29.7, 200 x 64 22.5 / 19.4; FP4, 1 x 1024 6.7 / 7.8, 16 x 4096 24.3 / 26.8,
+  // 64 x 1024 23.0 / 28.7, 64 x 256 to 2048 35.0 / 32.4, 200 x 512 34.4 / 42.6.
   const int per = (tiles + cluster - 1) / cluster;
   if (pairs <= 3 * static_cast<int64_t>(fit) && per <= 8 && per <= pairs * (tiles + 1) / fit + 3) {
     resident_ctas<decode_kernel<T, D, NT, FP4, true>>(smem, &e);
     if (e != cudaSuccess) return e;
     p.cluster = cluster;
-    cfg.gridDim = dim3(static_cast<unsigned>(pairs * cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<T, D, NT, FP4, true>, p);
+    return launch_dependent(decode_kernel<T, D, NT, FP4, true>, dim3(static_cast<unsigned>(pairs * cluster)), kThreads,
+                            smem, stream, p, cluster);
   }
   p.grid = max_grid < fit ? max_grid : fit;
   p.joins = static_cast<int>(pairs < p.grid ? pairs : p.grid);
-  decode_kernel<T, D, NT, FP4, false><<<p.grid, kThreads, smem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.c.capacity <= tile_keys(FP4, D)) return cudaSuccess;  // one tile per pair: none is split
-  cfg.gridDim = dim3(p.joins, p.chunk_heads);
-  cfg.blockDim = dim3(static_cast<int64_t>(p.joins) * p.chunk_heads <= 148 ? 16 * kMaxGroups : 128);
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, D, NT>, p);
+  e = launch_dependent(decode_kernel<T, D, NT, FP4, false>, dim3(p.grid), kThreads, smem, stream, p);
+  if (e != cudaSuccess || p.c.capacity <= tile_keys(FP4, D)) return e;  // one tile per pair: none is split
+  const bool few = static_cast<int64_t>(p.joins) * p.chunk_heads <= 148;
+  return launch_dependent(join_kernel<T, D, NT>, dim3(p.joins, p.chunk_heads), few ? 16 * kMaxGroups : 128, 0, stream, p);
 }
 
 template <typename T>
 cudaError_t launch_type(const DecodeParams& p, int D, bool fp4, int NT, int max_grid, cudaStream_t stream) {
-  if (D == 128) {
-    if (fp4) return NT == 1 ? launch_one<T, 128, 1, true>(p, max_grid, stream) : launch_one<T, 128, 2, true>(p, max_grid, stream);
-    return NT == 1 ? launch_one<T, 128, 1, false>(p, max_grid, stream) : launch_one<T, 128, 2, false>(p, max_grid, stream);
-  }
-  if (fp4) return NT == 1 ? launch_one<T, 64, 1, true>(p, max_grid, stream) : launch_one<T, 64, 2, true>(p, max_grid, stream);
-  return NT == 1 ? launch_one<T, 64, 1, false>(p, max_grid, stream) : launch_one<T, 64, 2, false>(p, max_grid, stream);
+  auto pick = [&](auto one, auto two) { return NT == 1 ? one(p, max_grid, stream) : two(p, max_grid, stream); };
+  if (D == 128)
+    return fp4 ? pick(launch_one<T, 128, 1, true>, launch_one<T, 128, 2, true>)
+               : pick(launch_one<T, 128, 1, false>, launch_one<T, 128, 2, false>);
+  return fp4 ? pick(launch_one<T, 64, 1, true>, launch_one<T, 64, 2, true>)
+             : pick(launch_one<T, 64, 1, false>, launch_one<T, 64, 2, false>);
 }
 
 }  // namespace

@@ -86,6 +86,30 @@ struct DecodeParams {
   uint32_t* err;
 };
 
+// Launches of these kernels may begin while the stream's last kernel drains (programmatic dependent
+// launch; about 2 us less per call in a stream of them). Each waits for it first, before anything is read or
+// written.
+__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename P>
+inline cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
+                                    const P& p, unsigned cluster = 1) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // Keys of a CTA tile of the decode kernel: four warps with 16 (16-bit, D = 128) or 32 each.
 __host__ __device__ constexpr int tile_keys(bool fp4, int D) { return fp4 ? 128 : D == 64 ? 128 : 64; }
 constexpr int kMaxDecodeCtas = 1184;  // 8 per SM: bound of the decode grid and of its workspace

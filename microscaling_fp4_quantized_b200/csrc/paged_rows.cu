@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
   constexpr int LPR = D / 16, GPW = 32 / LPR;
     constexpr int kUnroll = FP4 ? 2 : 4;
   constexpr bool kAhead = FP4;
+  wait_for_stream();
   const int lane = threadIdx.x & 31, j = lane % LPR;
   const int items = p.items_q + p.items_k + p.items_v;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
@@ -271,10 +272,17 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
   if (ok && rot) {
     const float* row = p.rope + static_cast<int64_t>(at.pos) * R;
     const int oa = INTER ? 4 * ca : 8 * ca, ob = INTER ? 4 * cb : 8 * ca + 4;
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + oa)), c1 = __ldg(reinterpret_cast<const float4*>(row + ob));
-    const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + R / 2 + oa)), s1 = __ldg(reinterpret_cast<const float4*>(row + R / 2 + ob));
-    cs[0] = make_float2(c0.x, c0.y); cs[1] = make_float2(c0.z, c0.w); cs[2] = make_float2(c1.x, c1.y); cs[3] = make_float2(c1.z, c1.w);
-    sn[0] = make_float2(s0.x, s0.y); sn[1] = make_float2(s0.z, s0.w); sn[2] = make_float2(s1.x, s1.y); sn[3] = make_float2(s1.z, s1.w);
+    const float* cos_sin[2] = {row, row + R / 2};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(cos_sin[k] + oa));
+      const float4 b4 = __ldg(reinterpret_cast<const float4*>(cos_sin[k] + ob));
+      float2* to = k == 0 ? cs : sn;
+      to[0] = make_float2(a.x, a.y);
+      to[1] = make_float2(a.z, a.w);
+      to[2] = make_float2(b4.x, b4.y);
+      to[3] = make_float2(b4.z, b4.w);
+    }
   }
   const void* wp = set == 0 ? p.qw : set == 1 ? p.kw : nullptr;
   float2 wa[4], wb[4];
@@ -430,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
 template <typename T, int D, bool FP4>
 __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const GatherParams p) {
   constexpr int LPR = D / 16, GPW = 32 / LPR, kUnroll = 4;
+  wait_for_stream();
   const int lane = threadIdx.x & 31, j = lane % LPR;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
   const int64_t tg = w / (2 * p.items);
@@ -497,14 +506,15 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const GatherParams 
 
 template <typename T, int D, bool INTER>
 static cudaError_t rows_of(const RowsParams& p, bool to_cache, bool fp4, unsigned grid, cudaStream_t stream) {
-  if (!to_cache) rows_kernel<T, D, false, false, INTER><<<grid, kThreads, 0, stream>>>(p);
-  else if (fp4) rows_kernel<T, D, true, true, INTER><<<grid, kThreads, 0, stream>>>(p);
-  else rows_kernel<T, D, true, false, INTER><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  auto* kernel = !to_cache ? rows_kernel<T, D, false, false, INTER>
+                 : fp4     ? rows_kernel<T, D, true, true, INTER>
+                           : rows_kernel<T, D, true, false, INTER>;
+  return launch_dependent(kernel, dim3(grid), kThreads, 0, stream, p);
 }
 
 template <typename T>
-static cudaError_t rows_of_type(const RowsParams& p, int D, bool to_cache, bool fp4, unsigned grid, cudaStream_t stream) {
+static cudaError_t rows_of_type(const RowsParams& p, int D, bool to_cache, bool fp4, unsigned grid,
+                                cudaStream_t stream) {
   if (D == 128)
     return p.interleaved ? rows_of<T, 128, true>(p, to_cache, fp4, grid, stream)
                          : rows_of<T, 128, false>(p, to_cache, fp4, grid, stream);
@@ -544,9 +554,8 @@ cudaError_t launch_rows(const RowsParams& in, int D, int dtype, bool to_cache, b
 }
 
 template <typename T, int D>
-static void gather_of(const GatherParams& p, bool fp4, unsigned grid, cudaStream_t stream) {
-  if (fp4) gather_kernel<T, D, true><<<grid, kThreads, 0, stream>>>(p);
-  else gather_kernel<T, D, false><<<grid, kThreads, 0, stream>>>(p);
+static cudaError_t gather_of(const GatherParams& p, bool fp4, unsigned grid, cudaStream_t stream) {
+  return launch_dependent(fp4 ? gather_kernel<T, D, true> : gather_kernel<T, D, false>, dim3(grid), kThreads, 0, stream, p);
 }
 
 cudaError_t launch_gather(const GatherParams& in, int D, int dtype, bool fp4, cudaStream_t stream) {
@@ -560,14 +569,9 @@ cudaError_t launch_gather(const GatherParams& in, int D, int dtype, bool fp4, cu
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(blocks);
-  if (dtype == kDtypeBF16) {
-    if (D == 128) gather_of<__nv_bfloat16, 128>(p, fp4, grid, stream);
-    else gather_of<__nv_bfloat16, 64>(p, fp4, grid, stream);
-  } else {
-    if (D == 128) gather_of<__half, 128>(p, fp4, grid, stream);
-    else gather_of<__half, 64>(p, fp4, grid, stream);
-  }
-  return cudaGetLastError();
+  if (dtype == kDtypeBF16)
+    return D == 128 ? gather_of<__nv_bfloat16, 128>(p, fp4, grid, stream) : gather_of<__nv_bfloat16, 64>(p, fp4, grid, stream);
+  return D == 128 ? gather_of<__half, 128>(p, fp4, grid, stream) : gather_of<__half, 64>(p, fp4, grid, stream);
 }
 
 }  // namespace sage
