@@ -47,12 +47,14 @@ struct Refused : std::exception {  // a ValueError or TypeError with a message
 };
 struct Raised : std::exception {};  // a Python error is already set
 
-void refuse_if(bool bad, const std::string& text) {
-  if (bad) throw Refused(text);
-}
+// (a macro: the message is put together only when it is needed)
+#define REFUSE_IF(bad, text)        \
+  do {                              \
+    if (bad) throw Refused((text)); \
+  } while (0)
 
 const char* name_of(at::ScalarType t) {
-  return t == at::kBFloat16 ? "torch.bfloat16" : t == at::kHalf ? "torch.float16" : t == at::kFloat ? "torch.float32" : "torch.int32";
+  return t == at::kBFloat16 ? "torch.bfloat16" : "torch.float16";
 }
 
 std::string where(at::Device d) { return d.str(); }
@@ -75,16 +77,18 @@ std::string text_of(at::IntArrayRef s) {
 }
 
 void check_rows(const char* name, const Tensor& t, int64_t dim, at::ScalarType dtype, at::Device dev) {
-  refuse_if(!t.is_cuda() || t.device() != dev, std::string(name) + " must be a CUDA tensor on " + where(dev));
-  refuse_if(t.dim() != dim, std::string(name) + " must have " + std::to_string(dim) + " dimensions");
-  refuse_if(t.scalar_type() != dtype, std::string(name) + " must be " + name_of(dtype));
-  refuse_if(t.size(dim - 1) != 1 && t.stride(dim - 1) != 1, std::string(name) + ": the channel (last) dimension must be contiguous");
+  REFUSE_IF(!t.is_cuda() || t.device() != dev, std::string(name) + " must be a CUDA tensor on " + where(dev));
+  REFUSE_IF(t.dim() != dim, std::string(name) + " must have " + std::to_string(dim) + " dimensions");
+  REFUSE_IF(t.scalar_type() != dtype, std::string(name) + " must be " + name_of(dtype));
+  REFUSE_IF(t.size(dim - 1) != 1 && t.stride(dim - 1) != 1,
+            std::string(name) + ": the channel (last) dimension must be contiguous");
 }
 
 void check_table(const char* name, const Tensor& t, at::IntArrayRef shape, at::Device dev) {
-  refuse_if(!t.is_cuda() || t.device() != dev || t.scalar_type() != at::kInt,
+  REFUSE_IF(!t.is_cuda() || t.device() != dev || t.scalar_type() != at::kInt,
             std::string(name) + " must be an int32 CUDA tensor on " + where(dev));
-  refuse_if(!shape_is(t, shape) || !t.is_contiguous(), std::string(name) + " must be contiguous with shape " + text_of(shape));
+  REFUSE_IF(!shape_is(t, shape) || !t.is_contiguous(),
+            std::string(name) + " must be contiguous with shape " + text_of(shape));
 }
 
 sage_dtype_t code_of(at::ScalarType t) {
@@ -102,19 +106,20 @@ bool make_rope(sage_fp4_rope_t* r, int64_t D, at::ScalarType dtype, at::Device d
   const char* const names[2] = {"q_weight", "k_weight"};
   for (int i = 0; i < 2; ++i) {
     if (w[i] == nullptr) continue;
-    refuse_if(!w[i]->is_cuda() || w[i]->device() != dev || !shape_is(*w[i], {D}) || !w[i]->is_contiguous(),
+    REFUSE_IF(!w[i]->is_cuda() || w[i]->device() != dev || !shape_is(*w[i], {D}) || !w[i]->is_contiguous(),
               std::string(names[i]) + " must be a contiguous [" + std::to_string(D) + "] CUDA tensor on " + where(dev));
     const at::ScalarType t = w[i]->scalar_type();
-    refuse_if((t != dtype && t != at::kFloat) || (i == 1 && qw != nullptr && qw->scalar_type() != t),
+    REFUSE_IF((t != dtype && t != at::kFloat) || (i == 1 && qw != nullptr && qw->scalar_type() != t),
               std::string("norm weights must both be ") + name_of(dtype) + " or both float32");
     r->weight_f32 = t == at::kFloat;
     (i == 0 ? r->q_weight : r->k_weight) = w[i]->data_ptr();
   }
   r->eps = static_cast<float>(eps);
   if (rope != nullptr) {
-    refuse_if(!rope->is_cuda() || rope->device() != dev || rope->scalar_type() != at::kFloat || rope->dim() != 2 || !rope->is_contiguous(),
+    REFUSE_IF(!rope->is_cuda() || rope->device() != dev || rope->scalar_type() != at::kFloat || rope->dim() != 2 ||
+                  !rope->is_contiguous(),
               "rope must be a contiguous float32 CUDA tensor [positions, rotary_dim] on " + where(dev));
-    refuse_if(rope->size(0) > INT32_MAX || rope->size(1) > INT32_MAX, "rope is too large");
+    REFUSE_IF(rope->size(0) > INT32_MAX || rope->size(1) > INT32_MAX, "rope is too large");
     // A table of no positions has no address; any aligned one says that there is a table.
     r->rope = rope->numel() > 0 ? static_cast<const float*>(rope->data_ptr()) : reinterpret_cast<const float*>(16);
     r->rope_len = static_cast<int>(rope->size(0));
@@ -125,7 +130,7 @@ bool make_rope(sage_fp4_rope_t* r, int64_t D, at::ScalarType dtype, at::Device d
 }
 
 int to_int(int64_t v, const char* what) {
-  refuse_if(v > INT32_MAX, std::string(what) + " is too large");
+  REFUSE_IF(v > INT32_MAX, std::string(what) + " is too large");
   return static_cast<int>(v);
 }
 
@@ -149,9 +154,10 @@ const Cache& cache_of(PyObject* o) {
 }
 
 sage_fp4_batch_t make_batch(const Cache& c, const Tensor& table, const Tensor& lens, const Tensor* cu) {
-  refuse_if(!table.is_cuda() || table.device() != c.device || table.scalar_type() != at::kInt,
+  REFUSE_IF(!table.is_cuda() || table.device() != c.device || table.scalar_type() != at::kInt,
             "page_table must be an int32 CUDA tensor on " + where(c.device));
-  refuse_if(table.dim() != 2 || (table.size(1) > 1 && table.stride(1) != 1), "page_table must be [sequences, pages] with contiguous rows");
+  REFUSE_IF(table.dim() != 2 || (table.size(1) > 1 && table.stride(1) != 1),
+            "page_table must be [sequences, pages] with contiguous rows");
   const int64_t B = table.size(0);
   check_table("seq_lens", lens, {B}, c.device);
   if (cu != nullptr) check_table("cu_seqlens", *cu, {B + 1}, c.device);
@@ -168,9 +174,9 @@ sage_fp4_batch_t make_batch(const Cache& c, const Tensor& table, const Tensor& l
 // total < 0: any number of rows.
 void check_dense(const char* name, const Tensor& t, const Cache& c, int64_t total) {
   check_rows(name, t, 3, c.dtype, c.device);
-  refuse_if(t.size(1) != c.c.Hkv || t.size(2) != c.c.D || (total >= 0 && t.size(0) != total),
-            std::string(name) + " must be [" + (total >= 0 ? std::to_string(total) : std::string("tokens")) + ", " + std::to_string(c.c.Hkv) + ", " +
-                std::to_string(c.c.D) + "]");
+  REFUSE_IF(t.size(1) != c.c.Hkv || t.size(2) != c.c.D || (total >= 0 && t.size(0) != total),
+            std::string(name) + " must be [" + (total >= 0 ? std::to_string(total) : std::string("tokens")) + ", " +
+                std::to_string(c.c.Hkv) + ", " + std::to_string(c.c.D) + "]");
 }
 
 Tensor empty_rows(at::IntArrayRef shape, at::ScalarType dtype, at::Device dev) {
@@ -204,7 +210,7 @@ PyObject* guarded(PyObject* const*, Py_ssize_t n, Py_ssize_t want, F f) {
   HANDLE_TH_ERRORS
   try {
     if (n != want) throw Refused("wrong number of arguments", PyExc_TypeError);
-    refuse_if(g.decode == nullptr, "the library is not bound");
+    REFUSE_IF(g.decode == nullptr, "the library is not bound");
     return f();
   } catch (const Refused& e) {
     PyErr_SetString(e.type, e.text.c_str());
@@ -243,8 +249,8 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dims[1] = hnd ? 1 : 2;
       dims[2] = hnd ? 2 : 1;
     } else {
-      refuse_if(q.dim() != 3, "q must be [B, H, N, D] ('HND'), [B, N, H, D] ('NHD') or [tokens, H, D]");
-      refuse_if(rope != nullptr && pos == nullptr, "packed rows need positions");
+      REFUSE_IF(q.dim() != 3, "q must be [B, H, N, D] ('HND'), [B, N, H, D] ('NHD') or [tokens, H, D]");
+      REFUSE_IF(rope != nullptr && pos == nullptr, "packed rows need positions");
     }
     const int64_t rank = q.dim(), D = q.size(rank - 1);
     const at::Device dev = q.device();
@@ -254,10 +260,10 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t B = dims[0] >= 0 ? q.size(0) : 1, N = q.size(dims[2]);
     if (k != nullptr) {
       check_rows("k", *k, rank, dtype, dev);
-      refuse_if(k->size(rank - 1) != D || k->size(dims[2]) != N || (dims[0] >= 0 && k->size(0) != B),
+      REFUSE_IF(k->size(rank - 1) != D || k->size(dims[2]) != N || (dims[0] >= 0 && k->size(0) != B),
                 "q and k disagree on batch, tokens or head dimension");
     } else {
-      refuse_if(ko != nullptr || kw != nullptr, "k_out and k_weight need k");
+      REFUSE_IF(ko != nullptr || kw != nullptr, "k_out and k_weight need k");
     }
     if (pos != nullptr) {
       if (dims[0] >= 0) check_table("positions", *pos, {B, N}, dev);
@@ -268,7 +274,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     auto output = [&](const char* name, const Tensor& x, const Tensor* y) {
       if (y == nullptr) return empty_rows(x.sizes(), dtype, dev);
       check_rows(name, *y, rank, dtype, dev);
-      refuse_if(y->sizes() != x.sizes(), std::string(name) + " must have the shape of its input");
+      REFUSE_IF(y->sizes() != x.sizes(), std::string(name) + " must have the shape of its input");
       return *y;
     };
     const c10::cuda::CUDAGuard guard(dev);
@@ -278,8 +284,9 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const sage_fp4_rows_t qr = make_rows(q, q_out, dims);
     sage_fp4_rows_t kr;
     if (k != nullptr) kr = make_rows(*k, *k_out, dims);
-    check_status(g.norm_rope(&qr, k != nullptr ? &kr : nullptr, to_int(B, "the batch"), to_int(N, "the number of tokens"),
-                             to_int(D, "the head dimension"), code, some ? &r : nullptr,
+    check_status(g.norm_rope(&qr, k != nullptr ? &kr : nullptr, to_int(B, "the batch"),
+                             to_int(N, "the number of tokens"), to_int(D, "the head dimension"), code,
+                             some ? &r : nullptr,
                              pos != nullptr ? static_cast<const int32_t*>(pos->data_ptr()) : nullptr, stream_of(dev)),
                  "sage_fp4_norm_rope");
     return wrap_pair(q_out, k_out);
@@ -290,7 +297,8 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(a, n, 13, [&]() -> PyObject* {
     const Cache& c = cache_of(a[0]);
-    const Tensor &k = *tensor(a[1], "k"), &v = *tensor(a[2], "v"), &table = *tensor(a[3], "page_table"), &lens = *tensor(a[4], "seq_lens");
+    const Tensor &k = *tensor(a[1], "k"), &v = *tensor(a[2], "v");
+    const Tensor &table = *tensor(a[3], "page_table"), &lens = *tensor(a[4], "seq_lens");
     const Tensor* cu = tensor_or_none(a[5], "cu_seqlens");
     const Tensor* q = tensor_or_none(a[6], "q");
     const Tensor *qw = tensor_or_none(a[7], "q_weight"), *kw = tensor_or_none(a[8], "k_weight");
@@ -302,7 +310,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check_dense("k", k, c, -1);
     const int64_t total = k.size(0);
     check_dense("v", v, c, total);
-    refuse_if(cu == nullptr && total != b.B, "without cu_seqlens, k and v hold one token per sequence");
+    REFUSE_IF(cu == nullptr && total != b.B, "without cu_seqlens, k and v hold one token per sequence");
     sage_fp4_rope_t r;
     const bool some = make_rope(&r, c.c.D, c.dtype, c.device, qw, kw, eps, rope, inter);
     const c10::cuda::CUDAGuard guard(c.device);
@@ -310,22 +318,22 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     sage_fp4_rows_t rows;
     if (q != nullptr) {
       check_rows("q", *q, 3, c.dtype, c.device);
-      refuse_if(q->size(0) != total || q->size(2) != c.c.D,
+      REFUSE_IF(q->size(0) != total || q->size(2) != c.c.D,
                 "q must be [" + std::to_string(total) + ", heads, " + std::to_string(c.c.D) + "]");
       if (qo == nullptr) {
         q_out = empty_rows(q->sizes(), c.dtype, c.device);
       } else {
         check_rows("q_out", *qo, 3, c.dtype, c.device);
-        refuse_if(qo->sizes() != q->sizes(), "q_out must have the shape of q");
+        REFUSE_IF(qo->sizes() != q->sizes(), "q_out must have the shape of q");
         q_out = *qo;
       }
       rows = make_rows(*q, *q_out, {-1, 1, 0});
     } else {
-      refuse_if(qo != nullptr || qw != nullptr, "q_out and q_weight need q");
+      REFUSE_IF(qo != nullptr || qw != nullptr, "q_out and q_weight need q");
     }
     const int64_t ks[2] = {stride(k, 1), stride(k, 0)}, vs[2] = {stride(v, 1), stride(v, 0)};
-    check_status(g.append(&c.c, &b, k.data_ptr(), ks, v.data_ptr(), vs, to_int(total, "the number of tokens"), some ? &r : nullptr,
-                          q != nullptr ? &rows : nullptr, stream_of(c.device)),
+    check_status(g.append(&c.c, &b, k.data_ptr(), ks, v.data_ptr(), vs, to_int(total, "the number of tokens"),
+                          some ? &r : nullptr, q != nullptr ? &rows : nullptr, stream_of(c.device)),
                  "sage_fp4_cache_append");
     return q_out.has_value() ? THPVariable_Wrap(*q_out) : Py_NewRef(Py_None);
   });
@@ -339,16 +347,16 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* cu = tensor_or_none(a[3], "cu_seqlens");
     const Tensor *ko = tensor_or_none(a[5], "k_out"), *vo = tensor_or_none(a[6], "v_out");
     const sage_fp4_batch_t b = make_batch(c, table, lens, cu);
-    refuse_if((ko == nullptr) != (vo == nullptr), "pass both of k_out and v_out, or neither");
+    REFUSE_IF((ko == nullptr) != (vo == nullptr), "pass both of k_out and v_out, or neither");
     int64_t total;
     if (a[4] != Py_None) {
       total = PyLong_AsLongLong(a[4]);
       if (total == -1 && PyErr_Occurred()) throw Raised();
     } else {
-      refuse_if(ko == nullptr && cu != nullptr, "cu_seqlens needs total, the number of rows");
+      REFUSE_IF(ko == nullptr && cu != nullptr, "cu_seqlens needs total, the number of rows");
       total = ko != nullptr && ko->dim() > 0 ? ko->size(0) : b.B;
     }
-    refuse_if(total < 0 || (cu == nullptr && total != b.B), "without cu_seqlens there is one row per sequence");
+    REFUSE_IF(total < 0 || (cu == nullptr && total != b.B), "without cu_seqlens there is one row per sequence");
     const c10::cuda::CUDAGuard guard(c.device);
     Tensor k, v;
     if (ko == nullptr) {
@@ -391,25 +399,26 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (t == nullptr) continue;
       const char* name = t == &q ? "q" : "out";
       check_rows(name, *t, 3, c.dtype, c.device);
-      refuse_if(!shape_is(*t, {b.B, H, c.c.D}),
+      REFUSE_IF(!shape_is(*t, {b.B, H, c.c.D}),
                 std::string(name) + " must be [" + std::to_string(b.B) + ", heads, " + std::to_string(c.c.D) + "]");
     }
-    refuse_if(H % c.c.Hkv != 0, "the number of query heads must be a multiple of the cache's heads");
+    REFUSE_IF(H % c.c.Hkv != 0, "the number of query heads must be a multiple of the cache's heads");
     const int heads = to_int(H, "the number of heads");
     const c10::cuda::CUDAGuard guard(c.device);
     const Tensor out = out_ != nullptr ? *out_ : empty_rows(q.sizes(), c.dtype, c.device);
     Tensor own;
     if (ws == nullptr) {
       const size_t need = g.workspace(&c.c, &b, heads);
-      own = at::empty({static_cast<int64_t>(need > 0 ? need : 256)}, at::TensorOptions().dtype(at::kByte).device(c.device));
+      own = at::empty({static_cast<int64_t>(need > 0 ? need : 256)},
+                      at::TensorOptions().dtype(at::kByte).device(c.device));
       ws = &own;
     } else {
-      refuse_if(!ws->is_cuda() || ws->device() != c.device || ws->scalar_type() != at::kByte || !ws->is_contiguous(),
+      REFUSE_IF(!ws->is_cuda() || ws->device() != c.device || ws->scalar_type() != at::kByte || !ws->is_contiguous(),
                 "workspace must be a contiguous uint8 CUDA tensor on " + where(c.device));
     }
     const int64_t qs[2] = {stride(q, 0), stride(q, 1)}, os[2] = {stride(out, 0), stride(out, 1)};
-    check_status(g.decode(&c.c, &b, q.data_ptr(), qs, out.data_ptr(), os, heads, static_cast<float>(scale), ws->data_ptr(),
-                          static_cast<size_t>(ws->numel()), stream_of(c.device)),
+    check_status(g.decode(&c.c, &b, q.data_ptr(), qs, out.data_ptr(), os, heads, static_cast<float>(scale),
+                          ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(c.device)),
                  "sage_fp4_attn_decode");
     return THPVariable_Wrap(out);
   });

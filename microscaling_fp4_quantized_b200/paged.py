@@ -166,8 +166,9 @@ class PagedKVCache:
         self._h = _n().make_cache(ctypes.addressof(self._c), k.device.index)
 
     @classmethod
-    def empty(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
-              format: str = "16bit", tensor_layout: str = "HND", device="cuda") -> "PagedKVCache":
+    def empty(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+              dtype: torch.dtype = torch.bfloat16, format: str = "16bit", tensor_layout: str = "HND",
+              device="cuda") -> "PagedKVCache":
         """A cache on buffers of its own (not initialised: only appended tokens are ever read)."""
         if format not in CACHE_FORMAT:
             raise ValueError(f"format must be one of {tuple(CACHE_FORMAT)}")
@@ -194,7 +195,8 @@ def cache_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, page_tab
     too, into q_out (may be q), which is returned. Two tokens of a call must not share a slot. A page
     outside the cache, a negative position and one beyond the rotation table are reported by
     device_error(); such a token is left out."""
-    return _n().append(cache._h, k, v, page_table, seq_lens, cu_seqlens, q, q_weight, k_weight, eps, rope, interleaved, q_out)
+    return _n().append(cache._h, k, v, page_table, seq_lens, cu_seqlens, q, q_weight, k_weight, eps, rope, interleaved,
+                       q_out)
 
 
 def cache_gather(cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, *,
@@ -208,7 +210,8 @@ def cache_gather(cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.
     return _n().gather(cache._h, page_table, seq_lens, cu_seqlens, total, k_out, v_out)
 
 
-def decode_workspace_bytes(cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor, num_q_heads: int) -> int:
+def decode_workspace_bytes(cache: PagedKVCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                           num_q_heads: int) -> int:
     """Workspace of sageattn_decode for these shapes."""
     return _n().workspace(cache._h, page_table, seq_lens, num_q_heads)
 
