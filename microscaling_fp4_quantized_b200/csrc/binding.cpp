@@ -1,12 +1,12 @@
 // Python binding of the paged cache operators: argument checks, output allocation and the call of the C
-// entry point, all natively. A step of a running batch takes 3 to 8 us on the GPU; checking its dozen
-// arguments and filling the C structures through ctypes took 20 to 30 us of host time, this takes a
-// quarter of that. The C functions are handed over by address (`bind`), so that the library
-// in use is the one the package has loaded.
+// entry point, all natively. A step of a running batch takes 3 to 7 us on the GPU; checking its dozen
+// arguments and filling the C structures through ctypes took 20 to 30 us of host time, this takes 5 (half of it
+// the launch, 0.6 for each tensor that is allocated). The C functions are handed over by address
+// (`bind`), so that the library in use is the one the package has loaded.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -180,7 +180,7 @@ void check_dense(const char* name, const Tensor& t, const Cache& c, int64_t tota
 }
 
 Tensor empty_rows(at::IntArrayRef shape, at::ScalarType dtype, at::Device dev) {
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(dev));
+  return Tensor(at::detail::empty_cuda(shape, dtype, dev, std::nullopt));
 }
 
 void* stream_of(at::Device dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
@@ -409,8 +409,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor own;
     if (ws == nullptr) {
       const size_t need = g.workspace(&c.c, &b, heads);
-      own = at::empty({static_cast<int64_t>(need > 0 ? need : 256)},
-                      at::TensorOptions().dtype(at::kByte).device(c.device));
+      own = empty_rows({static_cast<int64_t>(need > 0 ? need : 256)}, at::kByte, c.device);
       ws = &own;
     } else {
       REFUSE_IF(!ws->is_cuda() || ws->device() != c.device || ws->scalar_type() != at::kByte || !ws->is_contiguous(),
