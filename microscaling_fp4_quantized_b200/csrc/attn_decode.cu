@@ -301,6 +301,9 @@ __device__ __forceinline__ void values_fp4(const uint8_t* stage, int k0, int r, 
   }
 }
 
+// A partial result of no keys (scores that are all NaN leave the maximum at -inf too, but a sum of NaN).
+__device__ __forceinline__ bool nothing(float m, float sum) { return m == -INFINITY && sum == 0.0f; }
+
 // acc / sum (no keys: 0), rounded once.
 template <typename T, int N>
 __device__ __forceinline__ void store_out(T* out, const float (&acc)[N], float sum) {
@@ -825,7 +828,10 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
   }
   if constexpr (DIRECT) {
     if (p.cluster == 1) return;  // uniform over the grid
-    if (span <= 0 && tid < 8 * NT) part_ml[2 * tid] = -INFINITY;  // no tile here, no output
+    if (span <= 0 && tid < 8 * NT) {  // no tile here, no output
+      part_ml[2 * tid] = -INFINITY;
+      part_ml[2 * tid + 1] = 0.0f;
+    }
     cluster_sync();
     constexpr int Q = D / 4;  // a thread's piece: 4 channels of a head
     const int rank = blockIdx.x % p.cluster;
@@ -836,17 +842,17 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
       float mx = -INFINITY;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        ml[r].x = -INFINITY;
+        ml[r] = make_float2(-INFINITY, 0.0f);
         if (r < p.cluster) {
           ml[r] = ld_cluster2(part_ml + 2 * h, r);
-          if (ml[r].x != -INFINITY) v[r] = ld_cluster4(part_o + h * D + c0, r);
+          if (!nothing(ml[r].x, ml[r].y)) v[r] = ld_cluster4(part_o + h * D + c0, r);
         }
         mx = fmaxf(mx, ml[r].x);
       }
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        if (ml[r].x == -INFINITY) continue;
+        if (nothing(ml[r].x, ml[r].y)) continue;
         const float f = ex2_approx(ml[r].x - mx);
         sum += ml[r].y * f;
         acc[0] += v[r].x * f;
@@ -888,6 +894,7 @@ __global__ void __launch_bounds__(16 * kMaxGroups) join_kernel(const __grid_cons
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       m[u] = -INFINITY;
+      l[u] = 0.0f;
       if (first + G * u <= rec.w) {
         const int64_t row = row_of(first + G * u);
         const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + row * 2);
@@ -899,7 +906,7 @@ __global__ void __launch_bounds__(16 * kMaxGroups) join_kernel(const __grid_cons
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (m[u] == -INFINITY) continue;  // none, or an empty share, which has no output
+      if (nothing(m[u], l[u])) continue;  // none, or an empty share, which has no output
       const float top = fmaxf(mx, m[u]);
       const float f0 = mx == -INFINITY ? 0.0f : ex2_approx(mx - top), f1 = ex2_approx(m[u] - top);
       mx = top;

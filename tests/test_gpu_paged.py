@@ -580,6 +580,28 @@ def test_decode_nan_in_cached_token_reaches_only_its_sequence(sage, oracle_mod):
     assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
 
 
+@pytest.mark.parametrize("fmt", ["16bit", "fp4"])
+@pytest.mark.parametrize("lens,width", [([9000, 70], 1024), ([900, 70], 64), ([40, 3], 4)])
+def test_decode_nan_queries_and_keys(sage, oracle_mod, fmt, lens, width):
+    """A query that is not a number gives outputs that are not, however its sequence is split; the others are untouched.
+    A key that is not (16-bit) takes its heads with it."""
+    c = Case(sage, lens, 16, 2, 64, BF, fmt, width=width).fill(oracle_mod, 75)
+    q = randn(gen(76), 2, 6, 64)
+    want = sage.sageattn_decode(q, c.cache, c.table, c.seq_lens)
+    check_decode(c, q, want)
+    bad = q.clone()
+    bad[0, 4, 9] = float("nan")
+    out = sage.sageattn_decode(bad, c.cache, c.table, c.seq_lens)
+    assert torch.isnan(out[0, 4]).all()
+    out[0, 4] = want[0, 4]
+    assert torch.equal(out, want)
+    if fmt == "16bit":
+        page, slot, _ = c.places(c.lens)
+        c.k[page[lens[0] - 2], 1, slot[lens[0] - 2], 5] = float("nan")
+        out = sage.sageattn_decode(q, c.cache, c.table, c.seq_lens)
+        assert torch.isnan(out[0, 3:]).all() and torch.equal(out[0, :3], want[0, :3]) and torch.equal(out[1], want[1])
+
+
 def test_decode_strided_queries_outputs_and_tables(sage, oracle_mod):
     c = Case(sage, [70, 130, 5], 16, 2, 128, BF).fill(oracle_mod, 81)
     big = randn(gen(82), 3, 12, 128)
