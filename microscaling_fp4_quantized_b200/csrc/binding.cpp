@@ -179,13 +179,31 @@ void check_dense(const char* name, const Tensor& t, const Cache& c, int64_t tota
                 std::to_string(c.c.Hkv) + ", " + std::to_string(c.c.D) + "]");
 }
 
+// Other Python threads run meanwhile: an allocation may wait for the device and a launch for room in its
+// queue, which may itself be waiting for a host function in Python.
+class Unlocked {
+  PyThreadState* s = PyEval_SaveThread();
+
+ public:
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(s); }
+};
+
 Tensor empty_rows(at::IntArrayRef shape, at::ScalarType dtype, at::Device dev) {
+  const Unlocked u;
   return Tensor(at::detail::empty_cuda(shape, dtype, dev, std::nullopt));
 }
 
 void* stream_of(at::Device dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
-void check_status(int status, const char* what) {
+template <typename F>
+void run(const char* what, F call) {
+  int status;
+  {
+    const Unlocked u;
+    status = call();
+  }
   if (status == SAGE_OK) return;
   PyObject* r = PyObject_CallFunction(g.check, "is", status, what);
   Py_XDECREF(r);
@@ -284,11 +302,11 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const sage_fp4_rows_t qr = make_rows(q, q_out, dims);
     sage_fp4_rows_t kr;
     if (k != nullptr) kr = make_rows(*k, *k_out, dims);
-    check_status(g.norm_rope(&qr, k != nullptr ? &kr : nullptr, to_int(B, "the batch"),
-                             to_int(N, "the number of tokens"), to_int(D, "the head dimension"), code,
-                             some ? &r : nullptr,
-                             pos != nullptr ? static_cast<const int32_t*>(pos->data_ptr()) : nullptr, stream_of(dev)),
-                 "sage_fp4_norm_rope");
+    const int b = to_int(B, "the batch"), t = to_int(N, "the number of tokens"), d = to_int(D, "the head dimension");
+    run("sage_fp4_norm_rope", [&] {
+      return g.norm_rope(&qr, k != nullptr ? &kr : nullptr, b, t, d, code, some ? &r : nullptr,
+                         pos != nullptr ? static_cast<const int32_t*>(pos->data_ptr()) : nullptr, stream_of(dev));
+    });
     return wrap_pair(q_out, k_out);
   });
 }
@@ -332,9 +350,11 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       REFUSE_IF(qo != nullptr || qw != nullptr, "q_out and q_weight need q");
     }
     const int64_t ks[2] = {stride(k, 1), stride(k, 0)}, vs[2] = {stride(v, 1), stride(v, 0)};
-    check_status(g.append(&c.c, &b, k.data_ptr(), ks, v.data_ptr(), vs, to_int(total, "the number of tokens"),
-                          some ? &r : nullptr, q != nullptr ? &rows : nullptr, stream_of(c.device)),
-                 "sage_fp4_cache_append");
+    const int t = to_int(total, "the number of tokens");
+    run("sage_fp4_cache_append", [&] {
+      return g.append(&c.c, &b, k.data_ptr(), ks, v.data_ptr(), vs, t, some ? &r : nullptr,
+                      q != nullptr ? &rows : nullptr, stream_of(c.device));
+    });
     return q_out.has_value() ? THPVariable_Wrap(*q_out) : Py_NewRef(Py_None);
   });
 }
@@ -369,8 +389,10 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
       v = *vo;
     }
     const int64_t ks[2] = {stride(k, 1), stride(k, 0)}, vs[2] = {stride(v, 1), stride(v, 0)};
-    check_status(g.gather(&c.c, &b, k.data_ptr(), ks, v.data_ptr(), vs, to_int(total, "total"), stream_of(c.device)),
-                 "sage_fp4_cache_gather");
+    const int t = to_int(total, "total");
+    run("sage_fp4_cache_gather", [&] {
+      return g.gather(&c.c, &b, k.data_ptr(), ks, v.data_ptr(), vs, t, stream_of(c.device));
+    });
     return wrap_pair(k, v);
   });
 }
@@ -416,9 +438,10 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 "workspace must be a contiguous uint8 CUDA tensor on " + where(c.device));
     }
     const int64_t qs[2] = {stride(q, 0), stride(q, 1)}, os[2] = {stride(out, 0), stride(out, 1)};
-    check_status(g.decode(&c.c, &b, q.data_ptr(), qs, out.data_ptr(), os, heads, static_cast<float>(scale),
-                          ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(c.device)),
-                 "sage_fp4_attn_decode");
+    run("sage_fp4_attn_decode", [&] {
+      return g.decode(&c.c, &b, q.data_ptr(), qs, out.data_ptr(), os, heads, static_cast<float>(scale),
+                      ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(c.device));
+    });
     return THPVariable_Wrap(out);
   });
 }
