@@ -151,7 +151,7 @@ class PagedKVCache:
                     raise ValueError("scales must have the codes' shape with D / 16 bytes per row")
                 if any(c.shape[d] > 1 and c.stride(d) != 8 * s.stride(d) for d in range(3)):
                     raise ValueError("scales must have an eighth of the codes' strides")
-        self.k, self.v, self.k_sf, self.v_sf = k, v, k_sf, v_sf
+        self._buffers = (k, v, k_sf, v_sf)
         self.format = "fp4" if fp4 else "16bit"
         self.dtype = dtype if fp4 else k.dtype
         self.tensor_layout = tensor_layout
@@ -164,6 +164,9 @@ class PagedKVCache:
                          ks, vs, self.num_pages, self.page_size, self.num_kv_heads, D, _sage._dtype_code(self.dtype),
                          CACHE_FORMAT[self.format])
         self._h = _n().make_cache(ctypes.addressof(self._c), k.device.index)
+
+    # The buffers, fixed for the cache's life: the calls hold their addresses.
+    k, v, k_sf, v_sf = (property(lambda self, i=i: self._buffers[i]) for i in range(4))
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
@@ -221,7 +224,7 @@ def sageattn_decode(q: torch.Tensor, cache: PagedKVCache, page_table: torch.Tens
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention of one new token per sequence, q [B, Hq, D], over the seq_lens[b] cached tokens of its sequence
     (its own key and value among them, once appended). Hq is a multiple of the cache's heads. A sequence
-    of length 0 gets zeros; out may be q. A length outside the page table is clamped and a page outside the cache counts
+    of length 0 gets zeros, and so does a head whose scores are all -inf; out may be q. A length outside the page table is clamped and a page outside the cache counts
     as zeros, both reported by device_error(). workspace: uint8, 256-byte aligned, of at least
     decode_workspace_bytes(); one that calls share must not serve two at once (allocated per call
     when left out)."""
@@ -236,7 +239,8 @@ def sageattn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: P
                      interleaved: bool = False, is_causal: bool = True, **attn) -> torch.Tensor:
     """Prompts into the cache and their attention: cache_append (with q), cache_gather, sageattn_varlen.
 
-    q [tokens, Hq, D], k, v [tokens, Hkv, D] packed by cu_seqlens; seq_lens as in cache_append. Prompts that
+    q [tokens, Hq, D], k, v [tokens, Hkv, D] packed by cu_seqlens, with no rows behind the last prompt (as
+    sageattn_varlen wants them); seq_lens as in cache_append. Prompts that
     continue a cached prefix attend to all of it: cu_seqlens_kv (offsets of the whole sequences, the sums of
     seq_lens), max_seqlen_kv and total_kv then describe the keys. Keys and values are read back from the
     cache, so the prompt sees what later tokens will see, an FP4 cache's rounding included. Further keyword
