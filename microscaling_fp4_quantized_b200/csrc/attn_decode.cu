@@ -45,9 +45,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kMaxCluster = 8;  // the portable size
 constexpr int kThreads = 32 * kWarps;
-// Probabilities are kept as 2^kShift exp2(s - m): fp16 then keeps 11 bits for weights down to 2^-22
-// of the maximum, and the largest (2^kShift 2^4) is far from its limit. The factor cancels in the end.
-constexpr float kShift = 8.0f, kSlack = 4.0f;
+// Probabilities are kept as 2^shift exp2(s - m), the factor cancels in the end. fp16: 2^8, so that weights
+// down to 2^-22 of the maximum keep 11 bits and the largest (2^8 2^4) is far from its limit. bf16: 2^-16, so
+// that sums over values at the type's limit stay finite (2^12 keys of the largest weight); values
+// down to the smallest normal ones keep more bits than the output has.
+constexpr float kSlack = 4.0f;
 
 template <typename T>
 struct Is {
@@ -384,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
     decode_kernel(const __grid_constant__ DecodeParams p) {
   using S = Smem<D, FP4>;
   constexpr bool kMmaBf16 = Is<T>::bf16 && !FP4;  // FP4 values are exact in fp16
+  constexpr float kShift = kMmaBf16 ? -16.0f : 8.0f;
   constexpr int KS = D / 16;                      // contraction steps of S^T, channel tiles of O^T
   constexpr int KW = S::kKeys, G = KW / 16;       // keys of a warp and tile, in groups of 16
   // All shared memory is this array: behind any static one it would begin off a 128-byte line, and the copies into
