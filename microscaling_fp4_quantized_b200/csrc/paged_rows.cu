@@ -169,8 +169,10 @@ __device__ __forceinline__ Place place_of(const CacheView& c, int tok, bool lead
     first = __ldg(c.cu + b);
     const int end = __ldg(c.cu + b + 1);
     n = end - first;
-    if (tok < first || tok >= end) {  // rows behind the last sequence; before the first: a bad table
-      if (tok < first && lead) atomicOr(err, kDevErrSeqlens);
+    // Rows behind the last sequence; before the first, or a negative offset (with which the differences below
+    // could leave 32 bits): a bad table.
+    if (first < 0 || tok < first || tok >= end) {
+      if ((first < 0 || tok < first) && lead) atomicOr(err, kDevErrSeqlens);
       return r;
     }
   } else if (b >= c.B) {
@@ -209,7 +211,7 @@ __device__ __forceinline__ Place place_of(const CacheView& c, int tok, bool lead
 template <typename T, int D, bool CACHE, bool FP4, bool INTER>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int LPR = D / 16, GPW = 32 / LPR;
-    constexpr int kUnroll = FP4 ? 2 : 4;
+  constexpr int kUnroll = FP4 ? 2 : 4;
   constexpr bool kAhead = FP4;
   wait_for_stream();
   const int lane = threadIdx.x & 31, j = lane % LPR;

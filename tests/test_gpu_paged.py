@@ -9,6 +9,7 @@ attention adds its own terms (decode_tolerance). FP4 codes and scales, copies an
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -447,7 +448,8 @@ def test_bad_tables_are_reported_and_not_followed(sage, oracle_mod, fmt):
     # lengths outside the table, tokens at negative positions, offsets that do not rise
     q_out.fill_(7.0)
     for bad_lens, cu in (([33, 20, 20, 20], [0, 20, 20, 20, 20]), ([-5, 20, 20, 20], [0, 2, 2, 2, 2]),
-                         ([3, 20, 20, 20], [0, 9, 9, 9, 9]), ([20, 20, 20, 20], [5, 5, 5, 5, 5])):
+                         ([3, 20, 20, 20], [0, 9, 9, 9, 9]), ([20, 20, 20, 20], [5, 5, 5, 5, 5]),
+                         ([20, 20, 20, 20], [-2 ** 31, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1])):
         before = c.k.clone().view(torch.uint8)
         sage.cache_append(c.cache, k[:9], v[:9], c.table, torch.tensor(bad_lens, dtype=torch.int32).cuda(),
                           cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(), q=q[:9], q_out=q_out[:9])
@@ -559,6 +561,22 @@ def test_decode_identical_values_and_one_key(sage, oracle_mod):
         out = sage.sageattn_decode(randn(gen(52), 2, 8, 64, dtype=HF), c.cache, c.table, c.seq_lens)
         assert torch.equal(out[1], v[1].expand(8, 64))
         assert ((out[0] - v[0]).abs().double() <= 2 * U[HF] * v[0].abs().double()).all()
+
+
+@pytest.mark.parametrize("dtype,size", [(BF, 3.38e38), (BF, 2.0 ** -126), (HF, 65504.0), (HF, 2.0 ** -24)])
+@pytest.mark.parametrize("lens,width", [([1, 900], 64), ([1, 9000], 1024)])
+def test_decode_values_at_the_limits(sage, oracle_mod, dtype, size, lens, width):
+    """Values at the type's largest and smallest magnitudes, of both signs per channel: an average of equal
+    values neither overflows nor vanishes."""
+    c = Case(sage, lens, 16, 2, 64, dtype, width=width).fill(oracle_mod, 65)
+    row = torch.where(torch.arange(64) % 3 == 0, -size, size).to(dtype).cuda()
+    page, slot, _ = c.places(c.lens)
+    put(c.v, page, slot, "HND", row)
+    c.kv64 = [(k, row.double().expand(v.shape)) for k, v in c.kv64]
+    q = randn(gen(66), 2, 6, 64, dtype=dtype) * 0.05  # weights of like size: sums over many keys
+    out = sage.sageattn_decode(q, c.cache, c.table, c.seq_lens)
+    assert torch.equal(out[0], row.expand(6, 64))
+    check_decode(c, q, out)
 
 
 def test_decode_large_queries_on_fp4(sage, oracle_mod):
@@ -813,6 +831,45 @@ def test_prompt_continued_prompt_and_tokens(sage, oracle_mod, fmt):
         kk, vv = sage.cache_gather(c.cache, c.table, lens, cu_seqlens=c.cu(n), total=sum(n))
         c.lens, c.kv64 = n, list(zip(kk.double().split(n), vv.double().split(n)))
         check_decode(c, q, got)
+
+
+@pytest.mark.parametrize("fmt", ["16bit", "fp4"])
+def test_padded_prompts(sage, fmt):
+    """Rows behind the last prompt, whatever they hold, change nothing in the cache; attention over packed
+    rows wants them cut off, and says so."""
+    lens, H, Hq, D = [70, 1, 33], 2, 4, 64
+    n, rope, g = sum(lens), sage.rope_table(128, 64), gen(141)
+    q, k, v = randn(g, n, Hq, D), randn(g, n, H, D), randn(g, n, H, D)
+    held = []
+    for pad in (0, 25):
+        c = Case(sage, lens, 16, H, D, BF, fmt)
+        qp, kp, vp = (torch.cat((t, torch.full((pad,) + t.shape[1:], float("nan"), dtype=BF, device="cuda")))
+                      for t in (q, k, v))
+        out = sage.sageattn_prefill(qp, kp, vp, c.cache, c.table, c.seq_lens, c.cu(lens), max(lens), rope=rope)
+        assert out.shape == qp.shape and sage.device_error() == (sage.DEV_ERR_SEQLENS if pad else 0)
+        held.append((c.k.view(torch.uint8).clone(), c.v.view(torch.uint8).clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*held))
+
+
+def test_two_threads_at_once(sage, oracle_mod):
+    """Calls from two Python threads, each on its own stream."""
+    c = Case(sage, [2000, 31, 500], 16, 8, 128).fill(oracle_mod, 151)
+    q = [randn(gen(152 + i), 3, 32, 128) for i in range(2)]
+    want = [sage.sageattn_decode(x, c.cache, c.table, c.seq_lens) for x in q]
+    torch.cuda.synchronize()
+    same = [0, 0]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                same[i] += int(torch.equal(sage.sageattn_decode(q[i], c.cache, c.table, c.seq_lens), want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == [50, 50]
 
 
 def test_refusals_on_the_gpu(sage):
