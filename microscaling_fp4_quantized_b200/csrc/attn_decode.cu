@@ -481,10 +481,11 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
       x.nt = tiles_of<FP4, D>(x.len);
     }
   };
-  const int my_key = warp * KW + lane % KW;  // of a tile; 16-bit: lanes 16 apart hold the same key
+  constexpr int KL = KW < 32 ? KW : 32, L = KW / KL;  // keys of a warp that are copied together, and how often
+  const int my_key = warp * KW + lane % KL;  // of a tile (KL = 16: lanes 16 apart hold the same key), and every 32nd on
   // The page of this lane's key, loaded one tile ahead (-1: no such key, or no such page).
-  auto page_of = [&](const Cursor& x) -> int {
-    const int pos = x.t * tile_keys(FP4, D) + my_key;
+  auto page_of = [&](const Cursor& x, int l) -> int {
+    const int pos = x.t * tile_keys(FP4, D) + my_key + 32 * l;
     if (pos >= x.len) return -1;
     const int page = __ldg(c.table + x.b * c.table_stride + div_by_page(c.page, pos));
     if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(c.num_pages)) {
@@ -500,14 +501,14 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
   const char* const v_src = static_cast<const char*>(c.v) + ch * 16;
   const uint32_t k_at = FP4 ? kk * S::kKey + (ch << 4) : kk * S::kKey + ((ch ^ (kk & 7)) << 4);
   const uint32_t v_at = !FP4 ? k_at : v_row(kk) * S::kKey + ((D == 128 ? ch ^ (v_row(kk) & 2) : ch) << 4);
-  auto copy_rows = [&](uint32_t ko, uint32_t vo, uint32_t stage, auto all) {
+  auto copy_rows = [&](uint32_t ko, uint32_t vo, uint32_t stage, [[maybe_unused]] uint32_t sf, auto all) {
     // ALL: every key is there, so the copies need no length of their own.
     constexpr bool ALL = decltype(all)::value;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const uint32_t lane_at = half ? v_at : k_at;
 #pragma unroll
-      for (int i = 0; i < KW / KPI; ++i) {
+      for (int i = 0; i < KL / KPI; ++i) {
         const uint32_t o = __shfl_sync(0xffffffffu, half ? vo : ko, i * KPI + kk);
         const bool valid = ALL || o != 0xffffffffu;
         // 16-bit: the part of the swizzle that i brings flips chunk bits (rows are multiples of 128 bytes)
@@ -519,49 +520,59 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
     }
     if constexpr (FP4) {
       const bool valid = ALL || ko != 0xffffffffu;
-      cp_async_small<S::kSf>(stage + S::kKs + lane * S::kSf, c.k_sf + static_cast<uint64_t>(valid ? ko : 0u) * 2, valid);
-      cp_async_small<S::kSf>(stage + S::kVs + lane * S::kSf, c.v_sf + static_cast<uint64_t>(valid ? vo : 0u) * 2, valid);
+      cp_async_small<S::kSf>(sf + S::kKs + lane * S::kSf, c.k_sf + static_cast<uint64_t>(valid ? ko : 0u) * 2, valid);
+      cp_async_small<S::kSf>(sf + S::kVs + lane * S::kSf, c.v_sf + static_cast<uint64_t>(valid ? vo : 0u) * 2, valid);
     }
   };
   // The same where the warp's keys lie one behind the other (consecutive slots of one page): one address, at
   // fixed distances from this lane's own key's, serves all copies of a kind. Measured (us): FP4 batch 81.2 -> 78.4,
   // one long FP4 sequence 42.7 -> 41.7; 16-bit caches, which are not bound by instructions, the same.
-  auto copy_run = [&](uint32_t ko, uint32_t vo, uint32_t stage) {
-    const int64_t back = static_cast<int64_t>(lane * 16) - (lane % KW) * S::kKey;
+  auto copy_run = [&](uint32_t ko, uint32_t vo, uint32_t stage, [[maybe_unused]] uint32_t sf) {
+    const int64_t back = static_cast<int64_t>(lane * 16) - (lane % KL) * S::kKey;
     const char* ks = static_cast<const char*>(c.k) + back + static_cast<uint64_t>(ko) * 16;
     const char* vs = static_cast<const char*>(c.v) + back + static_cast<uint64_t>(vo) * 16;
 #pragma unroll
-    for (int i = 0; i < KW / KPI; ++i) {
+    for (int i = 0; i < KL / KPI; ++i) {
       const uint32_t flip = FP4 ? 0 : ((KPI * i) & 7) << 4;
       cp_async16(stage + (k_at ^ flip) + i * KPI * S::kKey, ks + i * 512);
       cp_async16(stage + S::kV + (v_at ^ flip) + i * KPI * S::kKey, vs + i * 512);
     }
     if constexpr (FP4) {
-      cp_async_small<S::kSf>(stage + S::kKs + lane * S::kSf, c.k_sf + static_cast<uint64_t>(ko) * 2, true);
-      cp_async_small<S::kSf>(stage + S::kVs + lane * S::kSf, c.v_sf + static_cast<uint64_t>(vo) * 2, true);
+      cp_async_small<S::kSf>(sf + S::kKs + lane * S::kSf, c.k_sf + static_cast<uint64_t>(ko) * 2, true);
+      cp_async_small<S::kSf>(sf + S::kVs + lane * S::kSf, c.v_sf + static_cast<uint64_t>(vo) * 2, true);
     }
   };
-  auto copy_tile = [&](const Cursor& x, int page, uint32_t stage) {
-    if (x.t * tile_keys(FP4, D) + warp * KW >= x.len) return;
-    // This lane's key as row offsets in units of 16 bytes; all ones: no such key.
-    const uint32_t pos = x.t * tile_keys(FP4, D) + my_key;
-    const uint32_t slot = pos - div_by_page(c.page, pos) * c.page.d;
-    const uint32_t ko = page * p.ku[0] + x.hk * p.ku[1] + slot * p.ku[2];
-    const uint32_t vo = page * p.vu[0] + x.hk * p.vu[1] + slot * p.vu[2];
-    if (__all_sync(0xffffffffu, page >= 0)) {
-      if (p.run) copy_run(ko, vo, stage);
-      else copy_rows(ko, vo, stage, std::true_type{});
+  int page[L];
+  auto pages = [&]() {
+#pragma unroll
+    for (int l = 0; l < L; ++l) page[l] = page_of(pc, l);
+  };
+  auto copy_tile = [&](uint32_t stage) {
+    if (pc.t * tile_keys(FP4, D) + warp * KW >= pc.len) return;
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+      // This lane's key as row offsets in units of 16 bytes; all ones: no such key.
+      const uint32_t pos = pc.t * tile_keys(FP4, D) + my_key + 32 * l;
+      const uint32_t slot = pos - div_by_page(c.page, pos) * c.page.d;
+      const uint32_t ko = page[l] * p.ku[0] + pc.hk * p.ku[1] + slot * p.ku[2];
+      const uint32_t vo = page[l] * p.vu[0] + pc.hk * p.vu[1] + slot * p.vu[2];
+      const uint32_t at = stage + l * KL * S::kKey, sf = stage + l * KL * S::kSf;
+      if (__all_sync(0xffffffffu, page[l] >= 0)) {
+        if (p.run) copy_run(ko, vo, at, sf);
+        else copy_rows(ko, vo, at, sf, std::true_type{});
+      } else {
+        copy_rows(page[l] >= 0 ? ko : 0xffffffffu, page[l] >= 0 ? vo : 0xffffffffu, at, sf, std::false_type{});
+      }
     }
-    else copy_rows(page >= 0 ? ko : 0xffffffffu, page >= 0 ? vo : 0xffffffffu, stage, std::false_type{});
   };
 
-  int page = pc.at < span ? page_of(pc) : -1;
+  if (pc.at < span) pages();
 #pragma unroll
   for (int i = 0; i < S::kStages - 1; ++i) {
     if (pc.at < span) {
-      copy_tile(pc, page, ring + i * S::kStage);
+      copy_tile(ring + i * S::kStage);
       advance(pc);
-      if (pc.at < span) page = page_of(pc);
+      if (pc.at < span) pages();
     }
     cp_async_commit();
   }
@@ -613,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
     cp_async_wait<S::kStages - 2>();
     __syncwarp();  // this tile has arrived for every lane, and every lane has read the one before
     if (pc.at < span) {
-      copy_tile(pc, page, ring + fill * S::kStage);
+      copy_tile(ring + fill * S::kStage);
       advance(pc);
-      if (pc.at < span) page = page_of(pc);
+      if (pc.at < span) pages();
     }
     cp_async_commit();
     const int k0 = cc.t * tile_keys(FP4, D) + warp * KW;
@@ -658,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           top[n][e] = fmaxf(s[0][n][e], s[0][n][e + 2]);
-          if (G == 2) top[n][e] = fmaxf(top[n][e], fmaxf(s[G - 1][n][e], s[G - 1][n][e + 2]));
+#pragma unroll
+          for (int g = 1; g < G; ++g) top[n][e] = fmaxf(top[n][e], fmaxf(s[g][n][e], s[g][n][e + 2]));
           raise |= top[n][e] > rise[n][e];
         }
       if (__any_sync(0xffffffffu, raise)) {
@@ -980,7 +992,7 @@ int resident_ctas(int smem, cudaError_t* e) {
 template <typename T, int D, int NT, bool FP4>
 cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   constexpr int smem = Smem<D, FP4>::kBytes;
-  p.run = p.c.sk.n == D && p.c.sv.n == D && p.c.page.d % Smem<D, FP4>::kKeys == 0;
+  p.run = p.c.sk.n == D && p.c.sv.n == D && p.c.page.d % (Smem<D, FP4>::kKeys < 32 ? Smem<D, FP4>::kKeys : 32) == 0;
   cudaError_t e = cudaSuccess;
   const int fit = resident_ctas<decode_kernel<T, D, NT, FP4, false>>(smem, &e);
   if (e != cudaSuccess) return e;

@@ -111,7 +111,7 @@ inline cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, unsigned block
 }
 
 // Keys of a CTA tile of the decode kernel: four warps with 16 (16-bit, D = 128) or 32 each.
-__host__ __device__ constexpr int tile_keys(bool fp4, int D) { return fp4 ? 128 : D == 64 ? 128 : 64; }
+__host__ __device__ constexpr int tile_keys(bool fp4, int D) { return fp4 ? (D == 64 ? 256 : 128) : D == 64 ? 128 : 64; }
 constexpr int kMaxDecodeCtas = 1184;  // 8 per SM: bound of the decode grid and of its workspace
 
 cudaError_t launch_rows(const RowsParams& p, int D, int dtype, bool to_cache, bool fp4, cudaStream_t stream);
