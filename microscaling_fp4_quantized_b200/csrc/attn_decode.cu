@@ -9,25 +9,26 @@
 //
 // Work split. The tokens of all (sequence, key/value head) pairs are cut into tiles, laid end to
 // end and dealt to the CTAs (as many as fit the machine) in contiguous shares of equal cost, so
-// that neither ragged lengths nor few pairs leave SMs idle. A CTA finishes the pairs that lie
+// that neither ragged lengths nor few pairs leave SMs idle. Where the heads fill the machine evenly the shares are
+// of one head's tiles instead, and the CTAs of all heads with the same share run side by side (see launch_one). A CTA finishes the pairs that lie
 // inside its share and leaves the (at most two) that cross its borders as partial (max, sum, output)
 // triples; join_kernel adds those up in the order of the shares, so results do not depend on timing.
 // Small problems (see launch_one) take a cluster of up to 8 CTAs per pair instead, which joins its parts
 // through distributed shared memory, in one launch.
 //
-// Each of the four warps owns 16 or 32 keys of a tile and its own ring of cp.async stages, so
+// Each of the four warps owns 16, 32 or 64 keys of a tile and its own ring of cp.async stages, so
 // the main loop has no block barrier; the warps meet when a pair ends. Scores are formed transposed,
 // S^T = K Q^T with 16 keys by 8 query heads per mma.m16n8k16 (a tcgen05 tile has 128 rows, of which a
 // decode step fills at most 16): a group of 8 heads wastes nothing, and movmatrix turns S^T into
 // the operand of O^T = V^T P^T. The running maximum is raised only when a score exceeds it by
 // 2^4, checked by one vote per tile: probabilities then reach 2^4 times the scale they are kept at.
 //
-// Measured on one B200, joins included, share of the 6549 GB/s a copy reaches: 16-bit, 16 sequences of 256 to 16384
-// tokens, 32 heads on 8, D 128: 82.7 us, 6.11 TB/s (0.93). 16-bit, 8 sequences of 2000 to 8192, 16 heads, D 64: 33.1 us, 5.06
-// TB/s (0.77). FP4, 64 sequences of 128 to 8192, 32 heads on 8: 78.4 us, 4.17 TB/s (0.64); one sequence of 131071:
-// 41.7 us, 3.62 TB/s (0.55). FP4 is bound by the instructions that decode it, about 350 per 16 keys at 2.4 a
-// cycle and SM (one conversion and one scaling per two elements are 128 of them); a second launch, the
-// join, costs 2 to 4 us.
+// Measured on one B200, joins included, share of the 6549 GB/s a copy reaches: 16-bit, 16 sequences of
+// 256 to 16384 tokens, 32 heads on 8, D 128: 80.3 us, 6.28 TB/s (0.96). 16-bit, 8 sequences of 2000 to 8192,
+// 16 heads, D 64: 31.4 us, 5.34 TB/s (0.81). FP4, 64 sequences of 128 to 8192, 32 heads on 8: 78.5 us,
+// 4.16 TB/s (0.64), with D 64 50.8 us (0.49); one sequence of 131071: 40.7 us, 3.71 TB/s (0.57). FP4 is
+// bound by the instructions that decode it, about 330 per 16 keys (113 for V, 91 for K, 48 for the copies) at
+// 2.4 a cycle and SM; a second launch, the join, costs 2 to 4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
   pc.at = 0;
   int span;
   [[maybe_unused]] int64_t u0 = 0, W = 0;
-  [[maybe_unused]] int shares = 0;
+  [[maybe_unused]] int shares = 0, my_share = 0;
   [[maybe_unused]] bool by_pair = false;
   if constexpr (DIRECT) {
     const int pair = blockIdx.x / p.cluster, rank = blockIdx.x - pair * p.cluster;
@@ -422,18 +423,22 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
     int64_t* red = reinterpret_cast<int64_t*>(meet);  // (not in use yet): per warp, then where the share begins
     int64_t& s_before = red[kWarps];
     int64_t& s_b = red[kWarps + 1];
-    W = count_tiles<FP4, D>(c, red, &before, blockIdx.x == 0 ? p.err : nullptr) * HC;
+    // p.side > 1: the shares are of one head's tiles, and p.side = HC blocks with the same share, each of its own head
+    // (chunk), run side by side.
+    const int stacked = p.side > 1 ? 1 : HC;
+    my_share = blockIdx.x / p.side;
+    W = count_tiles<FP4, D>(c, red, &before, blockIdx.x == 0 ? p.err : nullptr) * stacked;
     // Never more shares than tiles: shares of nothing between others would be loaded by the join for nothing (4
     // sequences of 3555 to 16573 FP4 tokens, one head: 12.9 us with them, 10.8 without).
-    shares = static_cast<int>(min(static_cast<int64_t>(p.grid), W));
-    u0 = share(W, blockIdx.x, shares);
-    span = static_cast<int>(blockIdx.x) < shares ? static_cast<int>(share(W, blockIdx.x + 1, shares) - u0) : 0;
+    shares = static_cast<int>(min(static_cast<int64_t>(p.grid / p.side), W));
+    u0 = share(W, my_share, shares);
+    span = my_share < shares ? static_cast<int>(share(W, my_share + 1, shares) - u0) : 0;
     {
       const int per = (c.B + kThreads - 1) / kThreads;
       const int lo = min(c.B, tid * per), hi = min(c.B, lo + per);
       for (int b = lo; b < hi; ++b) {
         const int64_t n = tiles_of<FP4, D>(length_of(c, b, nullptr)) + kPairCost;
-        if (before * HC <= u0 && u0 < (before + n) * HC) {
+        if (before * stacked <= u0 && u0 < (before + n) * stacked) {
           s_b = b;
           s_before = before;
         }
@@ -446,9 +451,10 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
       pc.b = static_cast<int>(s_b);
       pc.len = length_of(c, pc.b, nullptr);
       pc.nt = tiles_of<FP4, D>(pc.len);
-      const int64_t in = u0 - s_before * HC;
-      const int hc = static_cast<int>(in / (pc.nt + kPairCost));
-      const int rest = static_cast<int>(in - static_cast<int64_t>(hc) * (pc.nt + kPairCost)) - kPairCost;
+      const int64_t in = u0 - s_before * stacked;
+      const int above = static_cast<int>(in / (pc.nt + kPairCost));  // (0 side by side)
+      const int hc = p.side > 1 ? blockIdx.x - my_share * p.side : above;
+      const int rest = static_cast<int>(in - static_cast<int64_t>(above) * (pc.nt + kPairCost)) - kPairCost;
       pc.t = max(rest, 0);
       pc.at = max(-rest, 0);
       pc.hk = hc / p.chunks;
@@ -472,10 +478,12 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
     if (DIRECT || x.t < x.nt) return;
     x.at += kPairCost;
     x.t = 0;
-    if (++x.chunk < p.chunks) return;
-    x.chunk = 0;
-    if (++x.hk < c.Hkv) return;
-    x.hk = 0;
+    if (p.side == 1) {
+      if (++x.chunk < p.chunks) return;
+      x.chunk = 0;
+      if (++x.hk < c.Hkv) return;
+      x.hk = 0;
+    }
     if (++x.b < c.B) {
       x.len = length_of(c, x.b, nullptr);
       x.nt = tiles_of<FP4, D>(x.len);
@@ -756,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
       int4 rec = make_int4(-1, 0, 0, 0);
       if (begun && !whole) {
         const int64_t end = u0 + at.at - at.t + at.nt;  // past the pair's last tile
-        rec = make_int4(at.b, at.hk * p.chunks + at.chunk, static_cast<int>(blockIdx.x),
+        rec = make_int4(at.b, at.hk * p.chunks + at.chunk, my_share,
                         static_cast<int>((end * shares - 1) / W));
       }
       p.rec[by_pair ? static_cast<int64_t>(at.b) * HC + at.hk * p.chunks + at.chunk : blockIdx.x] = rec;
@@ -898,7 +906,10 @@ __global__ void __launch_bounds__(16 * kMaxGroups) join_kernel(const __grid_cons
   if (rec.x < 0) return;
   const int hk = rec.y / p.chunks, chunk = rec.y - hk * p.chunks;
   if (h >= min(p.chunk_heads, p.group - chunk * p.chunk_heads)) return;
-  auto row_of = [&](int cta) { return (static_cast<int64_t>(cta) * 2 + (cta == rec.z ? 1 : 0)) * (8 * NT) + h; };
+  auto row_of = [&](int share) {
+    const int cta = p.side > 1 ? share * p.side + rec.y : share;
+    return (static_cast<int64_t>(cta) * 2 + (share == rec.z ? 1 : 0)) * (8 * NT) + h;
+  };
   float mx = -INFINITY, acc[N], sum = 0.0f;
 #pragma unroll
   for (int e = 0; e < N; ++e) acc[e] = 0.0f;
@@ -1016,6 +1027,21 @@ cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
                             smem, stream, p, cluster);
   }
   p.grid = max_grid < fit ? max_grid : fit;
+  const int HC = p.c.Hkv * p.chunks, groups = p.grid / HC;
+  p.side = 1;
+  // Shares of one head each, the heads side by side: their blocks read the same tokens' rows at the same time, so that
+  // a token's rows of all heads (adjacent in NHD order, where a head's 32 bytes of codes and 4 of scales are parts of the
+  // DRAM's and L2's units) and the page table are fetched once. It needs a multiple of HC blocks, and the
+  // rest of the machine stays idle: up to an eighth of it in NHD order, almost nothing otherwise. Measured by
+  // all heads' tiles end to end / side by side (us): FP4 D = 64, 10 sequences of 24078 to 78702 tokens, 56 heads on 8,
+  // NHD 211 / 99.7 (end to end it read 3.9 times its bytes from DRAM), HND 98.5 / 97.4; the same with D = 128 NHD
+  // 269 / 156; 16 sequences of 256 to 16384, 32 heads on 8: FP4 D = 128 NHD 46.3 / 41.9, HND 40.9 / 39.9, 16-bit
+  // D = 64 NHD 46.9 / 43.8, HND 43.6 / 43.1, D = 128 NHD 81.0 / 79.8, HND 82.0 / 80.5.
+  const bool nhd = p.c.sk.h < p.c.sk.n && p.c.sv.h < p.c.sv.n;
+  if (groups * HC * 64 >= p.grid * (nhd ? 56 : 63)) {
+    p.side = HC;
+    p.grid = groups * HC;
+  }
   p.joins = static_cast<int>(pairs < p.grid ? pairs : p.grid);
   e = launch_dependent(decode_kernel<T, D, NT, FP4, false>, dim3(p.grid), kThreads, smem, stream, p);
   if (e != cudaSuccess || p.c.capacity <= tile_keys(FP4, D)) return e;  // one tile per pair: none is split

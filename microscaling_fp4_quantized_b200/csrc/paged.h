@@ -82,7 +82,7 @@ struct DecodeParams {
   float* part_ml;      // [grid, 2, 8 * NT, 2]
   int4* rec;           // [joins] what is to be joined
   int run;             // a warp's keys are consecutive in memory (set by launch_decode)
-  int grid, joins, cluster;  // (set by launch_decode)
+  int grid, joins, cluster, side;  // (set by launch_decode; side: blocks that share a range of tokens, one per head)
   uint32_t* err;
 };
 
@@ -110,7 +110,8 @@ inline cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, unsigned block
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Keys of a CTA tile of the decode kernel: four warps with 16 (16-bit, D = 128) or 32 each.
+// Keys of a CTA tile of the decode kernel: four warps with 16 (16-bit, D = 128), 32, or 64 each (FP4, D = 64,
+// whose bytes per key are the fewest for the same work around them).
 __host__ __device__ constexpr int tile_keys(bool fp4, int D) { return fp4 ? (D == 64 ? 256 : 128) : D == 64 ? 128 : 64; }
 constexpr int kMaxDecodeCtas = 1184;  // 8 per SM: bound of the decode grid and of its workspace
 
