@@ -520,6 +520,25 @@ def test_decode_by_pairs_and_by_shares(sage, oracle_mod, fmt, B, Hkv, width):
     assert torch.equal(out, sage.sageattn_decode(q, c.cache, c.table, c.seq_lens, workspace=ws))
 
 
+@pytest.mark.parametrize("fmt,D", [("16bit", 64), ("16bit", 128), ("fp4", 64), ("fp4", 128)])
+@pytest.mark.parametrize("layout,Hkv,group,lens", [
+    ("HND", 8, 2, [3000, 0, 1, 129, 64, 700]), ("NHD", 8, 2, [3000, 0, 1, 129, 64, 700]),
+    ("HND", 24, 2, [0, 1500, 300]), ("NHD", 24, 2, [0, 1500, 300]),  # blocks left over
+    ("NHD", 3, 40, [2000, 33]), ("HND", 2, 33, [2000, 33]),          # heads of a group in several chunks
+    ("NHD", 100, 1, [500, 0, 90]), ("HND", 67, 3, [500, 1]), ("NHD", 601, 1, [200]),
+])
+def test_decode_heads_side_by_side_or_end_to_end(sage, oracle_mod, fmt, D, layout, Hkv, group, lens):
+    """Wide tables, so that the tokens are dealt in shares: of one head each, with the blocks of all heads side by
+    side, or, where the heads do not fill the machine, of all heads' tiles end to end."""
+    c = Case(sage, lens, 16, Hkv, D, BF, fmt, layout, seed=5, width=4096).fill(oracle_mod, 35)
+    q = randn(gen(36), len(lens), Hkv * group, D)
+    out = sage.sageattn_decode(q, c.cache, c.table, c.seq_lens)
+    check_decode(c, q, out)
+    ws = torch.full((sage.decode_workspace_bytes(c.cache, c.table, c.seq_lens, q.shape[1]),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    assert torch.equal(out, sage.sageattn_decode(q, c.cache, c.table, c.seq_lens, workspace=ws))
+
+
 @pytest.mark.parametrize("fmt", ["16bit", "fp4"])
 def test_decode_one_long_sequence(sage, oracle_mod, fmt):
     """More shares than any other case; the last tokens matter as much as the first."""
