@@ -9,9 +9,9 @@
 //
 // Work split. The tokens of all (sequence, key/value head) pairs are cut into tiles, laid end to
 // end and dealt to the CTAs (as many as fit the machine) in contiguous shares of equal cost, so
-// that neither ragged lengths nor few pairs leave SMs idle. Where the heads fill the machine evenly the shares are
-// of one head's tiles instead, and the CTAs of all heads with the same share run side by side (see launch_one). A CTA finishes the pairs that lie
-// inside its share and leaves the (at most two) that cross its borders as partial (max, sum, output)
+// that neither ragged lengths nor few pairs leave SMs idle. Where the heads fill the machine evenly
+// the shares are of one head's tiles instead, and the CTAs of all heads with the same share run side
+// by side (see launch_one). A CTA finishes the pairs that lie inside its share and leaves the (at most two) that cross its borders as partial (max, sum, output)
 // triples; join_kernel adds those up in the order of the shares, so results do not depend on timing.
 // Small problems (see launch_one) take a cluster of up to 8 CTAs per pair instead, which joins its parts
 // through distributed shared memory, in one launch.
@@ -1030,8 +1030,8 @@ cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   const int HC = p.c.Hkv * p.chunks, groups = p.grid / HC;
   p.side = 1;
   // Shares of one head each, the heads side by side: their blocks read the same tokens' rows at the same time, so that
-  // a token's rows of all heads (adjacent in NHD order, where a head's 32 bytes of codes and 4 of scales are parts of the
-  // DRAM's and L2's units) and the page table are fetched once. It needs a multiple of HC blocks, and the
+  // a token's rows of all heads (adjacent in NHD order, where a head's 32 bytes of codes and 4 of scales are
+  // parts of the DRAM's and L2's units) and the page table are fetched once. It needs a multiple of HC blocks, and the
   // rest of the machine stays idle: up to an eighth of it in NHD order, almost nothing otherwise. Measured by
   // all heads' tiles end to end / side by side (us): FP4 D = 64, 10 sequences of 24078 to 78702 tokens, 56 heads on 8,
   // NHD 211 / 99.7 (end to end it read 3.9 times its bytes from DRAM), HND 98.5 / 97.4; the same with D = 128 NHD

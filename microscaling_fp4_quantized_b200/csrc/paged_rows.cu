@@ -8,9 +8,9 @@
 // item; the arithmetic runs on two channels per instruction. All three operations are bound by HBM: each
 // row is read once and written once. Measured on one B200, share of the 6549 GB/s a copy
 // reaches: norm and rotation of B1 H24 N32768 D128 143 us, 5.73 TB/s (0.88); prompt of 8191 tokens, 32 + 8
-// heads, 31.3 us, 5.42 TB/s (0.83); append of 17,995 tokens, 32 query and 8 key/value heads, 92 us, 4.8 TB/s (0.73), to FP4
-// pages 88.5 us, 4.4 TB/s (0.67: the encoding's instructions); dense read of 131,481 cached FP4 tokens, 8 heads, 106 us, 6.08
-// TB/s (0.93).
+// heads, 31.3 us, 5.42 TB/s (0.83); append of 17,995 tokens, 32 query and 8 key/value heads, 92 us, 4.8 TB/s
+// (0.73), to FP4 pages 88.5 us, 4.4 TB/s (0.67: the encoding's instructions); dense read of 131,481 cached FP4
+// tokens, 8 heads, 106 us, 6.08 TB/s (0.93).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
