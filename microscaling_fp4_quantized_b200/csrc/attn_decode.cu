@@ -261,12 +261,12 @@ __device__ __forceinline__ void scores_fp4(const uint8_t* stage, int k0, int r, 
   }
 }
 
-// O^T += V^T P^T over 16 FP4 keys. Lane (r, t4) takes channels r D/8 .. of keys 2t, 2t+1, 2t+8, 2t+9;
+// O^T += V^T (P + P_lo)^T over 16 FP4 keys (TWO; else P holds both, in columns of their own). Lane (r, t4) takes channels r D/8 .. of keys 2t, 2t+1, 2t+8, 2t+9;
 // the operand wants two keys' values of one channel side by side, so the nibbles of two
 // keys are interleaved before they are decoded.
-template <int D, int NT>
+template <int D, int NT, bool TWO>
 __device__ __forceinline__ void values_fp4(const uint8_t* stage, int k0, int r, int t4, const uint32_t (&pb)[NT][2],
-                                           float (&o)[NT][D / 16][4]) {
+                                           const uint32_t (&pl)[NT][2], float (&o)[NT][D / 16][4]) {
   using S = Smem<D, true>;
   constexpr int W = D / 64;  // code words of a lane and key: 2 or 1
   uint32_t w[4][W], sc[2];
@@ -299,7 +299,10 @@ __device__ __forceinline__ void values_fp4(const uint8_t* stage, int k0, int r, 
       const uint32_t a[4] = {mul_f16x2(lo[0][e], sc[0]), mul_f16x2(hi[0][e], sc[0]), mul_f16x2(lo[1][e], sc[1]),
                              mul_f16x2(hi[1][e], sc[1])};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma16816<false>(o[n][4 * i + e], a, pb[n][0], pb[n][1]);
+      for (int n = 0; n < NT; ++n) {
+        mma16816<false>(o[n][4 * i + e], a, pb[n][0], pb[n][1]);
+        if constexpr (TWO) mma16816<false>(o[n][4 * i + e], a, pl[n][0], pl[n][1]);
+      }
     }
   }
 }
@@ -382,12 +385,15 @@ struct Cursor {
 
 // DIRECT: a cluster of p.cluster CTAs takes one pair, each an equal part of its tiles, and joins the parts through
 // distributed shared memory: no partials in global memory, no second launch.
-template <typename T, int D, int NT, bool FP4, bool DIRECT>
+// HT: query heads of a column tile, 8 or 4. With 4, columns 4 to 7 are the same heads once more, and take what the
+// rounding of their weights leaves; with 8 that is a second product.
+template <typename T, int D, int NT, int HT, bool FP4, bool DIRECT>
 __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2 : 3)
     decode_kernel(const __grid_constant__ DecodeParams p) {
   using S = Smem<D, FP4>;
   constexpr bool kMmaBf16 = Is<T>::bf16 && !FP4;  // FP4 values are exact in fp16
   constexpr float kShift = kMmaBf16 ? -16.0f : 8.0f;
+  static_assert(HT == 8 || (HT == 4 && NT == 1 && FP4));
   constexpr int KS = D / 16;                      // contraction steps of S^T, channel tiles of O^T
   constexpr int KW = S::kKeys, G = KW / 16;       // keys of a warp and tile, in groups of 16
   // All shared memory is this array: behind any static one it would begin off a 128-byte line, and the copies into
@@ -603,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
       heads = min(p.chunk_heads, p.group - cc.chunk * p.chunk_heads);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int h = n * 8 + r;
+        const int h = n * 8 + r % HT;
         const T* q = static_cast<const T*>(p.q) + cc.b * p.sqb + static_cast<int64_t>(head0 + (h < heads ? h : 0)) * p.sqh;
         float sc[2] = {1.0f, 1.0f};
         if constexpr (!FP4) {
@@ -705,9 +711,8 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        // Weights as operands. 16-bit: the rounded weight and, in an operand of its own, what the rounding left (the
-        // tensor cores have room: one rounding of bf16 alone is as large as the output's). FP4: fp16's 11
-        // bits are well below the cache's own rounding; the sum then takes the rounded weights.
+        // Weights as operands: the rounded weight and, in an operand or columns of its own, what the rounding left. One
+        // rounding alone would be as large as the output's (of bf16; of fp16 on FP4 caches).
         uint32_t pb[NT][2];
         [[maybe_unused]] uint32_t pl[NT][2];
 #pragma unroll
@@ -715,20 +720,18 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[g][n][e] = ex2_approx(fmaf(s[g][n][e], qs[n][e & 1], -shift[n][e & 1]));
           float h[4] = {s[g][n][0], s[g][n][1], s[g][n][2], s[g][n][3]};
-          pb[n][0] = movm_t(pack_p<kMmaBf16>(h[0], h[1]));
-          pb[n][1] = movm_t(pack_p<kMmaBf16>(h[2], h[3]));
-          if constexpr (!FP4) {
+          uint32_t w[2] = {pack_p<kMmaBf16>(h[0], h[1]), pack_p<kMmaBf16>(h[2], h[3])};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[e] = s[g][n][e] - h[e];
-            }
-            pl[n][0] = movm_t(pack_p<kMmaBf16>(h[0], h[1]));
-            pl[n][1] = movm_t(pack_p<kMmaBf16>(h[2], h[3]));
+          for (int e = 0; e < 4; ++e) h[e] = s[g][n][e] - h[e];
+          const uint32_t left[2] = {pack_p<kMmaBf16>(h[0], h[1]), pack_p<kMmaBf16>(h[2], h[3])};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = s[g][n][e];
+          for (int e = 0; e < 2; ++e) {
+            if constexpr (HT == 4) w[e] = t4 < 2 ? w[e] : left[e];
+            else pl[n][e] = movm_t(left[e]);
+            pb[n][e] = movm_t(w[e]);
           }
-          l[n][0] += h[0] + h[2];
-          l[n][1] += h[1] + h[3];
+          l[n][0] += s[g][n][0] + s[g][n][2];
+          l[n][1] += s[g][n][1] + s[g][n][3];
         }
         if constexpr (!FP4) {
 #pragma unroll
@@ -743,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
             }
           }
         } else {
-          values_fp4<D, NT>(stage_p, 16 * g, r, t4, pb, o);
+          values_fp4<D, NT, HT == 8>(stage_p, 16 * g, r, t4, pb, pl, o);
         }
       }
     }
@@ -768,6 +771,12 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
                         static_cast<int>((end * shares - 1) / W));
       }
       p.rec[by_pair ? static_cast<int64_t>(at.b) * HC + at.hk * p.chunks + at.chunk : blockIdx.x] = rec;
+    }
+    if constexpr (HT == 4) {  // columns 0 to 3 get the sums of both
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[0][k][e] += __shfl_xor_sync(0xffffffffu, o[0][k][e], 2);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -1000,12 +1009,12 @@ int resident_ctas(int smem, cudaError_t* e) {
   return known[dev];
 }
 
-template <typename T, int D, int NT, bool FP4>
+template <typename T, int D, int NT, int HT, bool FP4>
 cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   constexpr int smem = Smem<D, FP4>::kBytes;
   p.run = p.c.sk.n == D && p.c.sv.n == D && p.c.page.d % (Smem<D, FP4>::kKeys < 32 ? Smem<D, FP4>::kKeys : 32) == 0;
   cudaError_t e = cudaSuccess;
-  const int fit = resident_ctas<decode_kernel<T, D, NT, FP4, false>>(smem, &e);
+  const int fit = resident_ctas<decode_kernel<T, D, NT, HT, FP4, false>>(smem, &e);
   if (e != cudaSuccess) return e;
   const int64_t pairs = static_cast<int64_t>(p.c.B) * p.c.Hkv * p.chunks;
   const int tiles = p.c.capacity > 0 ? (p.c.capacity - 1) / tile_keys(FP4, D) + 1 : 1;
@@ -1020,10 +1029,10 @@ cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   // 64 x 1024 23.0 / 28.7, 64 x 256 to 2048 35.0 / 32.4, 200 x 512 34.4 / 42.6.
   const int per = (tiles + cluster - 1) / cluster;
   if (pairs <= 3 * static_cast<int64_t>(fit) && per <= 8 && per <= pairs * (tiles + 1) / fit + 3) {
-    resident_ctas<decode_kernel<T, D, NT, FP4, true>>(smem, &e);
+    resident_ctas<decode_kernel<T, D, NT, HT, FP4, true>>(smem, &e);
     if (e != cudaSuccess) return e;
     p.cluster = cluster;
-    return launch_dependent(decode_kernel<T, D, NT, FP4, true>, dim3(static_cast<unsigned>(pairs * cluster)), kThreads,
+    return launch_dependent(decode_kernel<T, D, NT, HT, FP4, true>, dim3(static_cast<unsigned>(pairs * cluster)), kThreads,
                             smem, stream, p, cluster);
   }
   p.grid = max_grid < fit ? max_grid : fit;
@@ -1043,20 +1052,26 @@ cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
     p.grid = groups * HC;
   }
   p.joins = static_cast<int>(pairs < p.grid ? pairs : p.grid);
-  e = launch_dependent(decode_kernel<T, D, NT, FP4, false>, dim3(p.grid), kThreads, smem, stream, p);
+  e = launch_dependent(decode_kernel<T, D, NT, HT, FP4, false>, dim3(p.grid), kThreads, smem, stream, p);
   if (e != cudaSuccess || p.c.capacity <= tile_keys(FP4, D)) return e;  // one tile per pair: none is split
   const bool few = static_cast<int64_t>(p.joins) * p.chunk_heads <= 148;
   return launch_dependent(join_kernel<T, D, NT>, dim3(p.joins, p.chunk_heads), few ? 16 * kMaxGroups : 128, 0, stream, p);
 }
 
+// FP4 caches with at most four heads a chunk: every head in two columns, so that the remainders of the weights cost no
+// product of their own. Measured, two columns / two products (us): FP4, 64 sequences of 128 to 8192 tokens, 32 heads on
+// 8, D 128 80.7 / 88.1, D 64 51.7 / 55.9; one sequence of 131071 41.2 / 45.1. 16-bit caches are not bound by the products.
+template <typename T, int D>
+cudaError_t launch_format(const DecodeParams& p, bool fp4, int NT, int max_grid, cudaStream_t stream) {
+  if (!fp4)
+    return NT == 1 ? launch_one<T, D, 1, 8, false>(p, max_grid, stream) : launch_one<T, D, 2, 8, false>(p, max_grid, stream);
+  if (p.chunk_heads <= 4) return launch_one<T, D, 1, 4, true>(p, max_grid, stream);
+  return NT == 1 ? launch_one<T, D, 1, 8, true>(p, max_grid, stream) : launch_one<T, D, 2, 8, true>(p, max_grid, stream);
+}
+
 template <typename T>
 cudaError_t launch_type(const DecodeParams& p, int D, bool fp4, int NT, int max_grid, cudaStream_t stream) {
-  auto pick = [&](auto one, auto two) { return NT == 1 ? one(p, max_grid, stream) : two(p, max_grid, stream); };
-  if (D == 128)
-    return fp4 ? pick(launch_one<T, 128, 1, true>, launch_one<T, 128, 2, true>)
-               : pick(launch_one<T, 128, 1, false>, launch_one<T, 128, 2, false>);
-  return fp4 ? pick(launch_one<T, 64, 1, true>, launch_one<T, 64, 2, true>)
-             : pick(launch_one<T, 64, 1, false>, launch_one<T, 64, 2, false>);
+  return D == 128 ? launch_format<T, 128>(p, fp4, NT, max_grid, stream) : launch_format<T, 64>(p, fp4, NT, max_grid, stream);
 }
 
 }  // namespace

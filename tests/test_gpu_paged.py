@@ -598,6 +598,33 @@ def test_decode_values_at_the_limits(sage, oracle_mod, dtype, size, lens, width)
     check_decode(c, q, out)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D,group,width", [(64, 4, None), (64, 12, 4096), (128, 4, 4096), (128, 12, None),
+                                           (64, 7, 4096), (128, 8, None), (128, 1, None)])
+def test_decode_weights_on_fp4_are_as_exact_as_on_16_bits(sage, dtype, D, group, width):
+    """Two kinds of keys, all of a kind alike, whose values nearly cancel: a rounding of the weights to 11 bits would
+    be the same for each of them and stand out in the sum (up to 1e-3 where 1.3e-4 and the output's rounding are
+    allowed). The bound is decode64's with what a second operand leaves of the weights' rounding."""
+    B, n, first = 6, 128, 53
+    c = Case(sage, [n] * B, 16, 1, D, dtype, "fp4", width=width)
+    g = gen(77)
+    kind = torch.stack([torch.randperm(n, generator=g, device="cuda") < first for _ in range(B)]).view(-1)
+    k = torch.zeros(B * n, 1, D, dtype=dtype, device="cuda")
+    k[~kind, 0, 0] = -6.0                       # codes and scales are exact
+    v = torch.where(kind, 6.0, -6.0).to(dtype)[:, None, None].expand(-1, 1, D).contiguous()
+    sage.cache_append(c.cache, k, v, c.table, c.seq_lens, cu_seqlens=c.cu(c.lens))
+    kk, vv = sage.cache_gather(c.cache, c.table, c.seq_lens, cu_seqlens=c.cu(c.lens), total=B * n)
+    assert torch.equal(kk, k) and torch.equal(vv, v)
+    q = torch.zeros(B, group, D, device="cuda")
+    q[..., 0] = 5.78 + 0.3 * (2 * torch.rand(B, group, generator=g, device="cuda") - 1)
+    q = q.to(dtype)
+    out = sage.sageattn_decode(q, c.cache, c.table, c.seq_lens, sm_scale=0.01)
+    for b in range(B):
+        want, amag, slack = decode64(q[b], k.double().view(B, n, 1, D)[b], v.double().view(B, n, 1, D)[b], 0.01)
+        tol = U[dtype] * want.abs() + (2 * U[HF] ** 2 * amag + slack) * (1 + U[dtype]) + TINY[dtype]
+        err = (out[b].double() - want).abs()
+        assert (err <= tol).all(), (b, float(err.max()), float((err / tol).max()))
+
 def test_decode_large_queries_on_fp4(sage, oracle_mod):
     """bf16 queries beyond fp16's range, and rows of very different size, are rescaled exactly."""
     c = Case(sage, [100], 16, 1, 128, BF, "fp4").fill(oracle_mod, 61)
