@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
@@ -592,9 +593,10 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
   }
 
   uint32_t qf[NT][KS][2];
-  // Per head column: the running maximum m (of scaled scores), the unscaled score that makes it rise, and the
-  // offset of the exponent.
-  float o[NT][KS][4], m[NT][2], rise[NT][2], shift[NT][2], l[NT][2], qs[NT][2];
+  // Per head column: the running maximum m and the score that makes it rise, both unscaled: a score's difference to m is
+  // taken before the scaling, so that it is exact near the maximum, however large the scores (scaled first, the step
+  // of binary32 beyond 2^26 would carry the best key's weight out of its type).
+  float o[NT][KS][4], m[NT][2], rise[NT][2], l[NT][2], qs[NT][2];
   uint32_t slot = 0, fill = S::kStages - 1;  // stages to read and to refill
   bool first = true;
   int head0 = pc.hk * p.group + pc.chunk * p.chunk_heads, heads = min(p.chunk_heads, p.group - pc.chunk * p.chunk_heads);
@@ -625,8 +627,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           qs[n][e] = fmaxf(p.scale_log2 * sc[e], 1.2e-38f);  // never 0: masked scores stay -inf
-          m[n][e] = rise[n][e] = -INFINITY;
-          shift[n][e] = -kShift;
+          m[n][e] = rise[n][e] = -FLT_MAX;                    // (finite: -inf - m stays -inf)
           l[n][e] = 0.0f;
         }
 #pragma unroll
@@ -696,11 +697,10 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x * qs[n][e], m[n][e]);
-            const float f = m[n][e] == -INFINITY ? 0.0f : ex2_approx(m[n][e] - x);
+            x = fmaxf(x, m[n][e]);
+            const float f = ex2_approx((m[n][e] - x) * qs[n][e]);
             m[n][e] = x;
-            rise[n][e] = (x + kSlack) / qs[n][e];
-            shift[n][e] = (x == -INFINITY ? 0.0f : x) - kShift;
+            rise[n][e] = __fadd_rd(x, kSlack / qs[n][e]);
             l[n][e] *= f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[g][n][e] = ex2_approx(fmaf(s[g][n][e], qs[n][e & 1], -shift[n][e & 1]));
+          for (int e = 0; e < 4; ++e) s[g][n][e] = ex2_approx(fmaf(s[g][n][e] - m[n][e & 1], qs[n][e & 1], kShift));
           float h[4] = {s[g][n][0], s[g][n][1], s[g][n][2], s[g][n][3]};
           uint32_t w[2] = {pack_p<kMmaBf16>(h[0], h[1]), pack_p<kMmaBf16>(h[2], h[3])};
 #pragma unroll
@@ -793,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
         if (r == 0 && pass == 0) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            meet_ml[(warp * 8 + 2 * t4 + e) * 2] = m[n][e];
+            // scaled, for the joining; -inf: no keys
+            meet_ml[(warp * 8 + 2 * t4 + e) * 2] = l[n][e] == 0.0f ? -INFINITY : fmaxf(m[n][e] * qs[n][e], -FLT_MAX);
             meet_ml[(warp * 8 + 2 * t4 + e) * 2 + 1] = l[n][e];
           }
         }

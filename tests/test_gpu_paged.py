@@ -625,6 +625,37 @@ def test_decode_weights_on_fp4_are_as_exact_as_on_16_bits(sage, dtype, D, group,
         err = (out[b].double() - want).abs()
         assert (err <= tol).all(), (b, float(err.max()), float((err / tol).max()))
 
+@pytest.mark.parametrize("fmt,dtype,size", [("16bit", BF, 2e3), ("16bit", BF, 3e4), ("16bit", HF, 6e3), ("fp4", BF, 3e4),
+                                            ("fp4", HF, 6e3)])
+@pytest.mark.parametrize("lens,width", [([100, 3], 16), ([2000, 700], 128), ([5000, 900], 4096)])
+def test_decode_scores_beyond_the_steps_of_32_bits(sage, oracle_mod, fmt, dtype, size, lens, width):
+    """Scores of 10^7 to 10^10, where a step of binary32 is many powers of e: the best key takes all (in the first
+    sequence it shares with its double in the second half). The next one is further below than decode64's bound on
+    the sums, and by more than 100 (heads where it is not are left out), so its weight is nothing."""
+    c = Case(sage, lens, 16, 2, 128, dtype, fmt, width=width).fill(oracle_mod, 45, scale=size / 4)
+    page, slot, _ = c.places(lens)
+    half = lens[0] // 2
+    for x in (c.k, c.ks) if fmt == "fp4" else (c.k,):
+        put(x, page[half:2 * half], slot[half:2 * half], "HND", x[page[:half], :, slot[:half]])
+    c.kv64[0][0][half:2 * half] = c.kv64[0][0][:half]
+    q = randn(gen(46), 2, 6, 128, dtype=dtype) * size
+    out = sage.sageattn_decode(q, c.cache, c.table, c.seq_lens, sm_scale=1.0)
+    assert torch.isfinite(out).all()
+    seen = 0
+    for b, n in enumerate(lens):
+        k, v = c.kv64[b]
+        many = 2 if b == 0 else 1
+        for h in range(6):
+            s = k[:, h // 3] @ q[b, h].double()
+            top, at = s.topk(many + 1)
+            bound = float((k[:, h // 3].abs() @ q[b, h].double().abs()).max()) * 136 * 2.0 ** -23
+            if top[many - 1] - top[many] <= bound + 100 or (many == 2 and top[0] != top[1]):
+                continue
+            seen += 1
+            mean = v[at[:many], h // 3].mean(0)
+            assert ((out[b, h].double() - mean).abs() <= U[dtype] * mean.abs() + TINY[dtype]).all(), (b, h)
+    assert seen >= 6
+
 def test_decode_large_queries_on_fp4(sage, oracle_mod):
     """bf16 queries beyond fp16's range, and rows of very different size, are rescaled exactly."""
     c = Case(sage, [100], 16, 1, 128, BF, "fp4").fill(oracle_mod, 61)
