@@ -49,9 +49,12 @@ constexpr int kMaxCluster = 8;  // the portable size
 constexpr int kThreads = 32 * kWarps;
 // Probabilities are kept as 2^shift exp2(s - m), the factor cancels in the end. fp16: 2^8, so that weights
 // down to 2^-22 of the maximum keep 11 bits and the largest (2^8 2^4) is far from its limit. bf16: 2^-16, so
-// that sums over values at the type's limit stay finite (2^12 keys of the largest weight); values
-// down to the smallest normal ones keep more bits than the output has.
+// that sums over values at the type's limit, which is binary32's, stay finite; when a lane's sum of weights passes
+// kFull, its warp halves its sums and all further weights. A warp's eight lanes then hold at most 8 (kFull + a tile's
+// 4 2^-12) of the largest value, about half. (Values at the other end, the smallest normal ones, keep more bits
+// than the output has over 2^15 keys a warp.) Parts are joined as averages, whose weights add up to one.
 constexpr float kSlack = 4.0f;
+constexpr float kFull = 0x1p-4f;
 
 template <typename T>
 struct Is {
@@ -176,7 +179,7 @@ struct Smem {
   static constexpr int kStages = !FP4 && D == 128 ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kMeet = kWarps * 4 * D * 4;  // four heads at a time
-  static constexpr int kBytes = kRing + kMeet + kWarps * 8 * 2 * 4;
+  static constexpr int kBytes = kRing + kMeet + kWarps * 8 * 3 * 4;
 };
 
 // Row of the V codes' stage that key `key` takes: a lane's keys 2t, 2t+1, 2t+8, 2t+9 lie in rows
@@ -308,21 +311,20 @@ __device__ __forceinline__ void values_fp4(const uint8_t* stage, int k0, int r, 
   }
 }
 
-// A partial result of no keys (scores that are all NaN leave the maximum at -inf too, but a sum of NaN).
-__device__ __forceinline__ bool nothing(float m, float sum) { return m == -INFINITY && sum == 0.0f; }
+// 1 / a sum of weights (2^-20 to 2^42), to 2 units in the last place; 0 of 0: no keys.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.0f ? 0.0f : __fdividef(1.0f, sum); }
 
-// acc / sum (no keys: 0), rounded once.
+// Rounds the output, once.
 template <typename T, int N>
-__device__ __forceinline__ void store_out(T* out, const float (&acc)[N], float sum) {
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+__device__ __forceinline__ void store_out(T* out, const float (&acc)[N]) {
   uint32_t w[N / 2];
 #pragma unroll
   for (int e = 0; e < N / 2; ++e) {
     if constexpr (Is<T>::bf16) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
       w[e] = *reinterpret_cast<const uint32_t*>(&v);
     } else {
-      w[e] = pack_half2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      w[e] = pack_half2(acc[2 * e], acc[2 * e + 1]);
     }
   }
   if constexpr (N == 8) *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -597,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
   // taken before the scaling, so that it is exact near the maximum, however large the scores (scaled first, the step
   // of binary32 beyond 2^26 would carry the best key's weight out of its type).
   float o[NT][KS][4], m[NT][2], rise[NT][2], l[NT][2], qs[NT][2];
+  [[maybe_unused]] float down = kShift;  // (bf16) the exponent of weights at the maximum
   uint32_t slot = 0, fill = S::kStages - 1;  // stages to read and to refill
   bool first = true;
   int head0 = pc.hk * p.group + pc.chunk * p.chunk_heads, heads = min(p.chunk_heads, p.group - pc.chunk * p.chunk_heads);
@@ -607,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
   while (cc.at < span) {
     if (first) {  // a new pair: its queries
       first = false;
+      down = kShift;
       head0 = cc.hk * p.group + cc.chunk * p.chunk_heads;
       heads = min(p.chunk_heads, p.group - cc.chunk * p.chunk_heads);
 #pragma unroll
@@ -687,6 +691,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
 #pragma unroll
           for (int g = 1; g < G; ++g) top[n][e] = fmaxf(top[n][e], fmaxf(s[g][n][e], s[g][n][e + 2]));
           raise |= top[n][e] > rise[n][e];
+          if constexpr (kMmaBf16) raise |= l[n][e] > kFull;
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -708,6 +713,23 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
               o[n][k][e + 2] *= f;
             }
           }
+        if constexpr (kMmaBf16) {
+          bool full = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) full |= l[n][0] > kFull || l[n][1] > kFull;
+          if (__any_sync(0xffffffffu, full)) {
+            down -= 1.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              l[n][0] *= 0.5f;
+              l[n][1] *= 0.5f;
+#pragma unroll
+              for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][k][e] *= 0.5f;
+            }
+          }
+        }
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -718,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[g][n][e] = ex2_approx(fmaf(s[g][n][e] - m[n][e & 1], qs[n][e & 1], kShift));
+          for (int e = 0; e < 4; ++e) s[g][n][e] = ex2_approx(fmaf(s[g][n][e] - m[n][e & 1], qs[n][e & 1], kMmaBf16 ? down : kShift));
           float h[4] = {s[g][n][0], s[g][n][1], s[g][n][2], s[g][n][3]};
           uint32_t w[2] = {pack_p<kMmaBf16>(h[0], h[1]), pack_p<kMmaBf16>(h[2], h[3])};
 #pragma unroll
@@ -794,8 +816,10 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             // scaled, for the joining; -inf: no keys
-            meet_ml[(warp * 8 + 2 * t4 + e) * 2] = l[n][e] == 0.0f ? -INFINITY : fmaxf(m[n][e] * qs[n][e], -FLT_MAX);
-            meet_ml[(warp * 8 + 2 * t4 + e) * 2 + 1] = l[n][e];
+            float* ml = meet_ml + (warp * 8 + 2 * t4 + e) * 3;
+            ml[0] = l[n][e] == 0.0f ? -INFINITY : fmaxf(m[n][e] * qs[n][e], -FLT_MAX);
+            ml[1] = l[n][e];
+            ml[2] = kMmaBf16 ? __int_as_float((127 + static_cast<int>(kShift - down)) << 23) : 1.0f;  // what halving took
           }
         }
         if ((t4 >> 1) == pass) {
@@ -817,15 +841,20 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
         const int hh = tid >> 5, h = pass * 4 + hh, c0 = (tid & 31) * N;
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, meet_ml[(w * 8 + h) * 2]);
-        float acc[N], sum = 0.0f;
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, meet_ml[(w * 8 + h) * 3]);
+        float acc[N], sum = 0.0f, wt[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float* ml = meet_ml + (w * 8 + h) * 3;
+          wt[w] = ml[0] == -INFINITY ? 0.0f : ml[2] * ex2_approx(ml[0] - mx);
+          sum += ml[1] * wt[w];
+        }
+        const float inv = inverse(sum);
 #pragma unroll
         for (int e = 0; e < N; ++e) acc[e] = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float mw = meet_ml[(w * 8 + h) * 2];
-          const float f = mw == -INFINITY ? 0.0f : ex2_approx(mw - mx);
-          sum += meet_ml[(w * 8 + h) * 2 + 1] * f;
+          const float f = wt[w] * inv;
           const float2* src = reinterpret_cast<const float2*>(meet + (w * 4 + hh) * D + c0);
 #pragma unroll
           for (int e = 0; e < N; e += 2) {
@@ -836,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
         if (n * 8 + h < heads) {
           if (whole) {
             T* out = static_cast<T*>(p.out) + at.b * p.sob + static_cast<int64_t>(head0 + n * 8 + h) * p.soh + c0;
-            store_out<T, N>(out, acc, sum);
+            store_out<T, N>(out, acc);
           } else if constexpr (DIRECT) {
             float2* po = reinterpret_cast<float2*>(part_o + (n * 8 + h) * D + c0);
 #pragma unroll
@@ -878,22 +907,27 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2
         ml[r] = make_float2(-INFINITY, 0.0f);
         if (r < p.cluster) {
           ml[r] = ld_cluster2(part_ml + 2 * h, r);
-          if (!nothing(ml[r].x, ml[r].y)) v[r] = ld_cluster4(part_o + h * D + c0, r);
+          if (ml[r].x != -INFINITY) v[r] = ld_cluster4(part_o + h * D + c0, r);
         }
         mx = fmaxf(mx, ml[r].x);
       }
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r) {
-        if (nothing(ml[r].x, ml[r].y)) continue;
-        const float f = ex2_approx(ml[r].x - mx);
-        sum += ml[r].y * f;
+        if (ml[r].x != -INFINITY) ml[r].y *= ex2_approx(ml[r].x - mx);
+        sum += ml[r].y;
+      }
+      const float inv = inverse(sum);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (ml[r].x == -INFINITY) continue;
+        const float f = ml[r].y * inv;
         acc[0] += v[r].x * f;
         acc[1] += v[r].y * f;
         acc[2] += v[r].z * f;
         acc[3] += v[r].w * f;
       }
-      store_out<T, 4>(static_cast<T*>(p.out) + pc.b * p.sob + static_cast<int64_t>(head0 + h) * p.soh + c0, acc, sum);
+      store_out<T, 4>(static_cast<T*>(p.out) + pc.b * p.sob + static_cast<int64_t>(head0 + h) * p.soh + c0, acc);
     }
     cluster_sync();  // the parts stay until every CTA has read them
   }
@@ -940,19 +974,33 @@ __global__ void __launch_bounds__(16 * kMaxGroups) join_kernel(const __grid_cons
         for (int e = 0; e < N / 4; ++e) v[u][e] = *reinterpret_cast<const float4*>(p.part_o + row * D + c0 + 4 * e);
       }
     }
+    // The average so far and the new ones, each by its share of the weights.
+    float top = mx;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);
+    if (top == -INFINITY) continue;  // empty shares
+    float f0 = mx == -INFINITY ? 0.0f : sum * ex2_approx(mx - top);
+    mx = top;
+    sum = f0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (nothing(m[u], l[u])) continue;  // none, or an empty share, which has no output
-      const float top = fmaxf(mx, m[u]);
-      const float f0 = mx == -INFINITY ? 0.0f : ex2_approx(mx - top), f1 = ex2_approx(m[u] - top);
-      mx = top;
-      sum = sum * f0 + l[u] * f1;
+      l[u] *= m[u] == -INFINITY ? 0.0f : ex2_approx(m[u] - top);
+      sum += l[u];
+    }
+    const float inv = inverse(sum);
+    f0 *= inv;
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] *= f0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (m[u] == -INFINITY) continue;  // none, or an empty share, which has no output
+      const float f = l[u] * inv;
 #pragma unroll
       for (int e = 0; e < N / 4; ++e) {
-        acc[4 * e] = acc[4 * e] * f0 + v[u][e].x * f1;
-        acc[4 * e + 1] = acc[4 * e + 1] * f0 + v[u][e].y * f1;
-        acc[4 * e + 2] = acc[4 * e + 2] * f0 + v[u][e].z * f1;
-        acc[4 * e + 3] = acc[4 * e + 3] * f0 + v[u][e].w * f1;
+        acc[4 * e] += v[u][e].x * f;
+        acc[4 * e + 1] += v[u][e].y * f;
+        acc[4 * e + 2] += v[u][e].z * f;
+        acc[4 * e + 3] += v[u][e].w * f;
       }
     }
   }
@@ -964,19 +1012,27 @@ __global__ void __launch_bounds__(16 * kMaxGroups) join_kernel(const __grid_cons
   }
   __syncthreads();
   if (g != 0) return;
-  for (int i = 0; i < G; ++i) mx = fmaxf(mx, s_ml[i][0]);
-  sum = 0.0f;
+  // The groups' averages by their shares of the weights: thread i (of 16) forms group i's.
+  const float m = tid < G ? s_ml[tid][0] : -INFINITY;
+  float wt = tid < G ? s_ml[tid][1] : 0.0f;
+  mx = m;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffu, mx, o));
+  wt = m == -INFINITY ? 0.0f : wt * ex2_approx(m - mx);
+  sum = wt;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffu, sum, o);
+  wt *= inverse(sum);
 #pragma unroll
   for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+#pragma unroll 8
   for (int i = 0; i < G; ++i) {
-    const float m = s_ml[i][0];
-    const float f = m == -INFINITY ? 0.0f : ex2_approx(m - mx);
-    sum += s_ml[i][1] * f;
+    const float f = __shfl_sync(0xffffu, wt, i);
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] += s_acc[i][c0 + e] * f;
   }
   const int64_t head = static_cast<int64_t>(hk) * p.group + chunk * p.chunk_heads + h;
-  store_out<T, N>(static_cast<T*>(p.out) + rec.x * p.sob + head * p.soh + c0, acc, sum);
+  store_out<T, N>(static_cast<T*>(p.out) + rec.x * p.sob + head * p.soh + c0, acc);
 }
 
 namespace {

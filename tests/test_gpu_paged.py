@@ -656,6 +656,29 @@ def test_decode_scores_beyond_the_steps_of_32_bits(sage, oracle_mod, fmt, dtype,
             assert ((out[b, h].double() - mean).abs() <= U[dtype] * mean.abs() + TINY[dtype]).all(), (b, h)
     assert seen >= 6
 
+@pytest.mark.parametrize("B,pages,first", [(1, 1024, False), (512, 1024, False), (512, 64, True)])
+def test_decode_sums_over_many_large_values(sage, B, pages, first):
+    """Values at bf16's limit, more of them than a sum of weights near one could hold: many parts of one sequence (1),
+    2^16 keys of one weight in each warp's sum (2), and 2^12 of them with 15 times the first keys' weight, which is
+    not yet enough to raise the running maximum (3). An average of equal values is that value; its binary32 sum
+    over n keys is off by at most n 2^-24 of it."""
+    D, P, n = 64, 256, 256 * pages
+    c = Case(sage, [2 * P], P, 1, D, BF)  # two pages, of which every sequence has many copies
+    row = torch.where(torch.arange(D) % 3 == 0, -3.38e38, 3.38e38).to(BF).cuda()
+    k = torch.zeros(2 * P, 1, D, dtype=BF, device="cuda")
+    k[P:, 0, 0] = 1.0
+    sage.cache_append(c.cache, k, row.expand(2 * P, 1, D).contiguous(), c.table, c.seq_lens, cu_seqlens=c.cu([2 * P]))
+    table = c.table[0, 1].expand(B, pages).contiguous()
+    table[:, 0] = c.table[0, 0]
+    q = torch.zeros(B, 1, D, dtype=BF, device="cuda")
+    if first:
+        q[..., 0] = 2.703125  # ln 2^3.9: exact in 8 bits
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    out = sage.sageattn_decode(q, c.cache, table, lens, sm_scale=1.0)
+    want = row.double()
+    assert torch.isfinite(out).all()
+    assert ((out.double() - want).abs() <= (U[BF] + n * 2.0 ** -24) * want.abs()).all()
+
 def test_decode_large_queries_on_fp4(sage, oracle_mod):
     """bf16 queries beyond fp16's range, and rows of very different size, are rescaled exactly."""
     c = Case(sage, [100], 16, 1, 128, BF, "fp4").fill(oracle_mod, 61)
