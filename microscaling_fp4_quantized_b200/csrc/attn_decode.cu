@@ -389,9 +389,11 @@ struct Cursor {
 // DIRECT: a cluster of p.cluster CTAs takes one pair, each an equal part of its tiles, and joins the parts through
 // distributed shared memory: no partials in global memory, no second launch.
 // HT: query heads of a column tile, 8 or 4. With 4, columns 4 to 7 are the same heads once more, and take what the
-// rounding of their weights leaves; with 8 that is a second product.
+// rounding of their weights leaves; with 8 that is a second product, whose operands do not fit 128 registers on FP4
+// with D = 128 (64 sequences of 128 to 8192 tokens, 64 heads on 8: four CTAs an SM 92.0 us, three 89.1; D = 64, where
+// they do, 57.7 and 58.7).
 template <typename T, int D, int NT, int HT, bool FP4, bool DIRECT>
-__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? 4 : D == 128 ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? (HT == 8 && D == 128 ? 3 : 4) : D == 128 ? 2 : 3)
     decode_kernel(const __grid_constant__ DecodeParams p) {
   using S = Smem<D, FP4>;
   constexpr bool kMmaBf16 = Is<T>::bf16 && !FP4;  // FP4 values are exact in fp16
