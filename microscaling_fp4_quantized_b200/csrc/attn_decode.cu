@@ -11,10 +11,11 @@
 // end and dealt to the CTAs (as many as fit the machine) in contiguous shares of equal cost, so
 // that neither ragged lengths nor few pairs leave SMs idle. Where the heads fill the machine evenly
 // the shares are of one head's tiles instead, and the CTAs of all heads with the same share run side
-// by side (see launch_one). A CTA finishes the pairs that lie inside its share and leaves the (at most two) that cross its borders as partial (max, sum, output)
-// triples; join_kernel adds those up in the order of the shares, so results do not depend on timing.
-// Small problems (see launch_one) take a cluster of up to 8 CTAs per pair instead, which joins its parts
-// through distributed shared memory, in one launch.
+// by side (see launch_one). A CTA finishes the pairs that lie inside its share and leaves the (at
+// most two) that cross its borders as parts (maximum, sum of weights, average); join_kernel weighs
+// those in the order of the shares, so results do not depend on timing. Small problems (see
+// launch_one) take a cluster of up to 8 CTAs per pair instead, which joins its parts through
+// distributed shared memory, in one launch.
 //
 // Each of the four warps owns 16, 32 or 64 keys of a tile and its own ring of cp.async stages, so
 // the main loop has no block barrier; the warps meet when a pair ends. Scores are formed transposed,

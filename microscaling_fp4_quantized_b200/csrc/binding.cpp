@@ -454,8 +454,13 @@ PyObject* make_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* p = PyLong_AsVoidPtr(a[0]);
   const long index = PyLong_AsLong(a[1]);
   if (PyErr_Occurred()) return nullptr;
+  const auto* given = static_cast<const sage_fp4_cache_t*>(p);
+  if (given->Hkv < 1 || given->page_size < 1) {  // the calls divide by both
+    PyErr_SetString(PyExc_ValueError, "a cache needs at least one head and one slot per page");
+    return nullptr;
+  }
   auto* c = new Cache;
-  std::memcpy(&c->c, p, sizeof(c->c));
+  c->c = *given;
   c->device = at::Device(at::kCUDA, static_cast<at::DeviceIndex>(index));
   c->dtype = c->c.dtype == SAGE_F16 ? at::kHalf : at::kBFloat16;
   PyObject* o = PyCapsule_New(c, kCapsule, free_cache);

@@ -1027,6 +1027,15 @@ def test_refusals_on_the_gpu(sage):
     assert e.value.status == sage.SAGE_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("layout", ["HND", "NHD"])
+@pytest.mark.parametrize("fmt", ["16bit", "fp4"])
+def test_caches_without_heads_or_slots_are_refused(sage, fmt, layout):
+    for pages, slots, heads in ((4, 16, 0), (4, 0, 2), (0, 16, 0)):
+        with pytest.raises(ValueError):
+            sage.PagedKVCache.empty(pages, slots, heads, 128, format=fmt, tensor_layout=layout)
+    sage.PagedKVCache.empty(0, 16, 2, 128, format=fmt, tensor_layout=layout)  # no pages yet: a cache like any other
+
+
 def test_empty_calls(sage):
     cache = sage.PagedKVCache.empty(4, 16, 2, 64)
     table, lens = torch.zeros(0, 3, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")

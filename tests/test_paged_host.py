@@ -98,6 +98,14 @@ def test_decode_refusals(sage, kw, status):
     assert decode(sage, **kw) == status
 
 
+@pytest.mark.parametrize("kw", [dict(Hkv=0), dict(Hkv=-2), dict(page_size=0)])
+def test_a_cache_without_heads_or_slots_gets_no_handle(sage, kw):
+    """The calls divide by both; a handle is made for caches that have them."""
+    with pytest.raises(ValueError):
+        sage.paged._n().make_cache(ctypes.addressof(make_cache(sage, **kw)), 0)
+    sage.paged._n().make_cache(ctypes.addressof(make_cache(sage)), 0)
+
+
 def test_append_and_gather_refusals(sage):
     L, c, b, st = sage.lib(), make_cache(sage), make_batch(sage), s2(128, 256)
 
