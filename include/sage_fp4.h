@@ -458,10 +458,11 @@ size_t sage_fp4_decode_workspace_bytes(const sage_fp4_cache_t* cache, const sage
 /*
  * Attention of one query per sequence over the cache: out[b, h] = softmax(sm_scale q[b, h] K^T) V
  * over the seq_lens[b] tokens of sequence b and the key/value head h / (Hq / Hkv). q and out are
- * [B, Hq, D] with strides of (sequence, head); out may be q. A sequence of length 0 gets zeros, and so
- * does a head whose scores are all -inf. Small problems run in one launch, by pairs of sequence and head;
- * else the batch's tokens are cut into equal shares, whatever the lengths, and the parts of a pair joined
- * by a second launch. Results do not depend on timing. workspace: 256-byte aligned, at least
+ * [B, Hq, D] with strides of (sequence, head); out may be q (with the same strides), otherwise the
+ * two must not overlap. A sequence of length 0 gets zeros, and so does a head whose scores are all
+ * -inf. Small problems run in one launch, by pairs of sequence and head; else the batch's tokens are
+ * cut into equal shares, whatever the lengths, and the parts of a pair joined by a second launch.
+ * Results do not depend on timing. workspace: 256-byte aligned, at least
  * sage_fp4_decode_workspace_bytes(); calls that may overlap need one each.
  */
 sage_status_t sage_fp4_attn_decode(const sage_fp4_cache_t* cache, const sage_fp4_batch_t* batch, const void* q,

@@ -257,9 +257,12 @@ sage_status_t sage_fp4_attn_decode(const sage_fp4_cache_t* cache, const sage_fp4
   if (!std::isfinite(sm_scale)) return SAGE_ERR_INVALID_ARG;
   if (d.max_grid == 0) return SAGE_OK;
   if (!aligned(q, 16) || !aligned(out, 16) || q_stride == nullptr || o_stride == nullptr) return SAGE_ERR_INVALID_ARG;
-  for (int i = 0; i < 2; ++i)
+  const int64_t counts[2] = {batch->B, Hq};
+  for (int i = 0; i < 2; ++i) {
     if (!valid_stride(q_stride[i], 8) || !valid_stride(o_stride[i], 8)) return SAGE_ERR_INVALID_ARG;
-  if (!apart(o_stride[0], batch->B, cache->D) || !apart(o_stride[1], Hq, cache->D)) return SAGE_ERR_INVALID_ARG;
+    if (!apart(o_stride[i], counts[i], cache->D)) return SAGE_ERR_INVALID_ARG;
+    if (q == out && counts[i] > 1 && q_stride[i] != o_stride[i]) return SAGE_ERR_INVALID_ARG;
+  }
   if (!aligned(workspace, 256) || ws_bytes < d.bytes) return SAGE_ERR_INVALID_ARG;
   sage::DecodeParams p;
   std::memset(&p, 0, sizeof(p));

@@ -224,10 +224,11 @@ def sageattn_decode(q: torch.Tensor, cache: PagedKVCache, page_table: torch.Tens
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention of one new token per sequence, q [B, Hq, D], over the seq_lens[b] cached tokens of its sequence
     (its own key and value among them, once appended). Hq is a multiple of the cache's heads. A sequence
-    of length 0 gets zeros, and so does a head whose scores are all -inf; out may be q. A length outside the page
-    table is clamped and a page outside the cache counts as zeros, both reported by device_error(). workspace: uint8, 256-byte aligned, of at least
-    decode_workspace_bytes(); one that calls share must not serve two at once (allocated per call
-    when left out)."""
+    of length 0 gets zeros, and so does a head whose scores are all -inf; out may be q itself (not another
+    view of its memory). A length outside the page table is clamped and a page outside the cache counts as
+    zeros, both reported by device_error(). workspace: uint8, 256-byte aligned, of at least
+    decode_workspace_bytes(); one that calls share must not serve two at once (allocated per call when
+    left out)."""
     return _n().decode(cache._h, q, page_table, seq_lens, sm_scale, out, workspace)
 
 

@@ -743,6 +743,20 @@ def test_decode_in_place(sage, oracle_mod):
         assert torch.equal(q, want)
 
 
+def test_decode_in_place_needs_the_same_strides(sage, oracle_mod):
+    c = Case(sage, [90, 64, 3, 1], 16, 2, 128).fill(oracle_mod, 87)
+    q = randn(gen(88), 4, 4, 128)
+    kept = q.clone()
+    with pytest.raises(sage.SageError) as e:
+        sage.sageattn_decode(q, c.cache, c.table, c.seq_lens, out=q.transpose(0, 1))
+    assert e.value.status == sage.SAGE_ERR_INVALID_ARG and torch.equal(q, kept)
+    # strides of a dimension of one do not count
+    want = sage.sageattn_decode(q[:1], c.cache, c.table[:1], c.seq_lens[:1])
+    out = q.as_strided((1, 4, 128), (8, 128, 1))
+    sage.sageattn_decode(q[:1], c.cache, c.table[:1], c.seq_lens[:1], out=out)
+    assert torch.equal(q[:1], want) and torch.equal(q[1:], kept[1:])
+
+
 def test_many_sequences(sage, oracle_mod):
     """More sequences than threads of a block, most of them short or empty; steps for all of them at once."""
     B = 5000

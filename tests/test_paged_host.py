@@ -106,6 +106,12 @@ def test_a_cache_without_heads_or_slots_gets_no_handle(sage, kw):
     sage.paged._n().make_cache(ctypes.addressof(make_cache(sage)), 0)
 
 
+def test_decode_in_place_with_other_strides_is_refused(sage):
+    """Output rows would lie on query rows that other blocks have yet to read."""
+    for qs, os in (((1024, 128), (128, 384)), ((1024, 128), (2048, 128)), ((1024, 128), (1024, 256)), ((0, 128), (1024, 128))):
+        assert decode(sage, qs=s2(*qs), os=s2(*os)) == INV, (qs, os)
+
+
 def test_append_and_gather_refusals(sage):
     L, c, b, st = sage.lib(), make_cache(sage), make_batch(sage), s2(128, 256)
 
