@@ -10,18 +10,23 @@ reported in the device error word and the access skipped).
 
     python -m microscaling_fp4_quantized_b200.build [--force] [--verbose] [--checks]
 
-``csrc/binding.cpp``, the native Python binding of the paged cache operators, becomes the extension
-module ``_binding.so`` next to it (g++, torch's headers and libraries; no CUDA code of its own).
+``csrc/binding.cpp``, the native Python binding of the paged cache operators, then becomes the extension
+module ``_binding.so`` next to it (g++, torch's headers and libraries; no CUDA code of its own). Without
+torch it is left out. It is built again when torch or Python changes: it uses torch's C++ interface,
+which is another one in every release.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -63,8 +68,13 @@ def up_to_date(lib: str = LIB) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, checks: bool = False) -> str:
-    lib = LIB_CHECKS if checks else LIB
+    lib = _build_library(force, verbose, checks)
     build_binding(force)
+    return lib
+
+
+def _build_library(force: bool, verbose: bool, checks: bool) -> str:
+    lib = LIB_CHECKS if checks else LIB
     if not force and up_to_date(lib):
         return lib
     bdir = BUILD + ("_checks" if checks else "")
@@ -97,27 +107,42 @@ def build(force: bool = False, verbose: bool = False, checks: bool = False) -> s
     return lib
 
 
-def build_binding(force: bool = False) -> str:
+def build_binding(force: bool = False) -> Optional[str]:
+    """The binding's path; None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        sys.stderr.write("torch is not installed: the Python binding is not built\n")
+        return None
     src = os.path.join(CSRC, "binding.cpp")
-    deps = (src, os.path.join(INCLUDE, "sage_fp4.h"), os.path.abspath(__file__))
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in deps):
-        return BINDING
-    import torch
-    troot = os.path.dirname(os.path.abspath(torch.__file__))
+    troot = os.path.dirname(os.path.abspath(spec.origin))
     tlib = os.path.join(troot, "lib")
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
-    tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", os.path.join(troot, "include"),
            "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), src,
            "-L", tlib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath," + tlib]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    # What the file is good for, kept beside the objects: times alone do not tell.
+    built_for = "\n".join([f"torch {importlib.metadata.version('torch')}",
+                           f"Python {sysconfig.get_config_var('SOABI')}"] + cmd[1:])
+    stamp = os.path.join(BUILD, "binding.txt")
+    deps = (src, os.path.join(INCLUDE, "sage_fp4.h"), os.path.abspath(__file__))
+    if (not force and os.path.exists(BINDING) and os.path.exists(stamp)
+            and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in deps)):
+        with open(stamp) as f:
+            if f.read() == built_for:
+                return BINDING
+    import torch
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    r = subprocess.run(cmd + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", tmp],
+                       capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("the binding did not build")
     os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(built_for)
     return BINDING
 
 
