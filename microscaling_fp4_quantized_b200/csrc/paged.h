@@ -56,6 +56,7 @@ struct RowsParams {
   const float* rope;
   int rope_len, R, interleaved;
   const int32_t* positions;
+  float minus_zero;               // -0, unknown to the compiler (set by launch_rows; see rows_kernel)
   CacheView c;
   uint32_t* err;
 };

@@ -396,12 +396,15 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const __grid_constant
       }
       if (rot) {
         // Products and sums each rounded on their own (no fused multiply-add), as a chain of
-        // elementwise operations rounds them: codes then agree bit for bit.
+        // elementwise operations rounds them: codes then agree bit for bit. A mul.rn.f32x2 is contracted with
+        // the sum behind it (243 of two million fp16 outputs differ), a fused product with a -0 that only
+        // the host knows is not, and rounds the same.
+        const float2 mz = make_float2(p.minus_zero, p.minus_zero);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 a = xa[i], c = xb[i];
-          xa[i] = sub2(mul2(a, cs[i]), mul2(c, sn[i]));
-          xb[i] = add2(mul2(c, cs[i]), mul2(a, sn[i]));
+          xa[i] = sub2(fma2(a, cs[i], mz), fma2(c, sn[i], mz));
+          xb[i] = add2(fma2(c, cs[i], mz), fma2(a, sn[i], mz));
         }
       }
       float x[16];  // channels of the two chunks in order
@@ -536,6 +539,7 @@ static int heads_of(int64_t groups, int heads, int waves) {
 
 cudaError_t launch_rows(const RowsParams& in, int D, int dtype, bool to_cache, bool fp4, cudaStream_t stream) {
   RowsParams p = in;
+  p.minus_zero = -0.0f;
   const int gpw = 512 / D;
   const int64_t groups = (static_cast<int64_t>(p.T) + gpw - 1) / gpw;
   const int most = heads_of(groups, p.Hq + p.Hk + p.Hv, to_cache ? 1 : 4);

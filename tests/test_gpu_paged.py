@@ -244,6 +244,20 @@ def test_norm_rope(sage, layout, B, N, Hq, Hkv, D, rot, inter, norm, dtype):
     assert got is q2 and none is None and torch.equal(q2, qo)
 
 
+@pytest.mark.parametrize("D,rot,inter", [(64, 64, False), (128, 128, True), (128, 96, False), (64, 32, True)])
+def test_rotation_rounds_every_step(sage, D, rot, inter):
+    """Without a norm a rotation is two products and their sum, each rounded to binary32, and the rounding to fp16: bit for
+    bit, over enough elements (two million) that a product left unrounded in the sum would show in hundreds of them."""
+    N, H = 4096, 1024 // D // 2
+    q, pos = randn(gen(7), N, H, D, dtype=HF), torch.arange(N, dtype=torch.int32, device="cuda")
+    rope = sage.rope_table(N, rot)
+    want = rows32(q, None, rope, pos, inter).to(HF).cuda()
+    assert torch.equal(sage.qk_norm_rope(q, rope=rope, positions=pos, interleaved=inter)[0], want)
+    c = Case(sage, [N], 16, H, D, HF)
+    sage.cache_append(c.cache, q, q, c.table, c.seq_lens, cu_seqlens=c.cu([N]), rope=rope, interleaved=inter)
+    assert torch.equal(c.at(c.k, [N]), want) and torch.equal(c.at(c.v, [N]), q)
+
+
 def test_norm_rope_default_positions_strides_and_weights(sage):
     g = gen(5)
     B, N, H, D = 2, 33, 4, 128
