@@ -486,6 +486,55 @@ def test_bad_tables_are_reported_and_not_followed(sage, oracle_mod, fmt):
         check_decode(c2, qd, out)
 
 
+@pytest.mark.parametrize("fmt", ["16bit", "fp4"])
+def test_left_out_tokens_leave_everything_as_it_was(sage, oracle_mod, fmt):
+    """Tokens that are reported, and rows behind the last sequence, change neither codes nor scales nor outputs; those
+    beside them in the same call go where they belong."""
+    c = Case(sage, [20, 20, 20, 20], 16, 2, 64, BF, fmt, width=2).fill(oracle_mod, 5)
+    g = gen(17)
+    buffers = (c.k, c.v, c.ks, c.vs) if fmt == "fp4" else (c.k, c.v)
+    whole = lambda: [x.clone().view(torch.uint8) for x in buffers]  # noqa: E731
+    good = c.table.clone()
+    bad_table = good.clone()
+    bad_table[1, 0], bad_table[3, 1] = -1, c.pages
+    rope19, low, top = sage.rope_table(19, 64), -2 ** 31, 2 ** 31 - 1
+    E_LEN, E_PAGE = sage.DEV_ERR_SEQLENS, sage.DEV_ERR_PAGES
+    same, none = [20] * 4, []
+    for table, lens, cu, rope, err, rows in (  # rows: (row, sequence, position) of what is written
+            (bad_table, same, [0, 20, 40, 60, 80], rope19, E_LEN | E_PAGE,
+             [(i, 0, i) for i in range(19)] + [(36 + i, 1, 16 + i) for i in range(3)] + [(40 + i, 2, i) for i in range(19)]
+             + [(60 + i, 3, i) for i in range(16)]),
+            (good, [33, 20, 20, 20], [0, 20, 20, 20, 20], None, E_LEN, none),
+            (good, [-5, 20, 20, 20], [0, 2, 2, 2, 2], None, E_LEN, none),
+            (good, [3, 20, 20, 20], [0, 9, 9, 9, 9], None, E_LEN, [(6, 0, 0), (7, 0, 1), (8, 0, 2)]),
+            (good, same, [5, 5, 5, 5, 5], None, E_LEN, none),
+            (good, same, [low, top, top, top, top], None, E_LEN, none),
+            (good, [low, top, 20, 20], [0, 1, 2, 2, 2], None, E_LEN, none),
+            (good, same, [0, 0, 3, 3, 3], None, 0, [(0, 1, 17), (1, 1, 18), (2, 1, 19)])):
+        total = 80 if cu[-1] == 80 else 9
+        k, v, q = randn(g, total, 2, 64), randn(g, total, 2, 64), randn(g, total, 4, 64)
+        q_out = torch.full_like(q, 7.0)
+        want = whole()
+        sage.cache_append(c.cache, k, v, table, torch.tensor(lens, dtype=torch.int32).cuda(),
+                          cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(), q=q, q_out=q_out, rope=rope)
+        assert sage.device_error() == err, (lens, cu)
+        row, b, pos = (torch.tensor([r[i] for r in rows], dtype=torch.long) for i in range(3))
+        page, slot = table.cpu()[b, pos // 16].long().cuda(), (pos % 16).cuda()
+        kd, vd = rows32(k.cpu()[row], None, rope, pos, False), v.float().cpu()[row]
+        new = []
+        if rows and fmt == "fp4":
+            codes, scales = zip(quantized(oracle_mod, kd), quantized(oracle_mod, vd))
+            new = [torch.from_numpy(x).cuda() for x in codes + scales]
+        elif rows:
+            new = [x.to(BF).cuda().view(torch.uint8) for x in (kd, vd)]
+        for x, y in zip(want, new):
+            put(x, page, slot, "HND", y)
+        assert all(torch.equal(x, y) for x, y in zip(whole(), want)), (lens, cu)
+        out = torch.full_like(q, 7.0).cpu()
+        out[row] = rows32(q.cpu()[row], None, rope, pos, False).to(BF)
+        assert torch.equal(q_out.cpu(), out), (lens, cu)
+
+
 # -------------------------------------------------------------------------------------- decode --
 
 DECODE = [
@@ -960,6 +1009,50 @@ def test_prompt_continued_prompt_and_tokens(sage, oracle_mod, fmt):
         c.lens, c.kv64 = n, list(zip(kk.double().split(n), vv.double().split(n)))
         check_decode(c, q, got)
 
+
+
+@pytest.mark.parametrize("precision", ["fp4", "8bit"])
+@pytest.mark.parametrize("fmt", ["16bit", "fp4"])
+@pytest.mark.parametrize("one,two", [([0, 0, 0], [150, 33, 1]), ([150, 33, 1], [40, 129, 70]),
+                                     ([128, 0, 16, 300], [1, 128, 5, 15])])
+def test_every_prompt_token_attends_up_to_itself(sage, oracle_mod, fmt, precision, one, two):
+    """The second part of each prompt over the cached first one. Keys are random signs, and the query of a token is its
+    own key and, a little stronger, the next one: after the rotation to their true positions the own key leads all earlier
+    ones by far (scores 181 against 24 z, z normal), and only the causal mask keeps the next one out. So a token's
+    output is its own value, and any other offset, position, length or prefix shows. The values are signs too: FP4 holds them as 6 E4M3(1/6) = 1.03125, the 8-bit
+    path to 2^-4, the FP4 cache to 2^-5 first; weights sum to one within 2^-4 (E4M3) and the others' stay
+    below 0.01: 0.2 in all, where another value is off by 2."""
+    H, Hq, D, P = 2, 8, 128, 16
+    n = [a + b for a, b in zip(one, two)]
+    c = Case(sage, n, P, H, D, BF, fmt)
+    g = gen(161)
+    rope = sage.rope_table(max(n), D)
+    sign = lambda *s: torch.randint(0, 2, s, generator=g, device="cuda").float() * 2 - 1  # noqa: E731
+    keys, values = [sign(m, H, D) for m in n], [sign(m, H, D) for m in n]
+    queries = []
+    for k in keys:
+        nxt = torch.cat((k[1:], torch.zeros_like(k[:1])))
+        queries.append((16 * (k + 1.1 * nxt)).repeat_interleave(Hq // H, dim=1))
+    part = lambda xs, lo, hi: torch.cat([x[a:b] for x, a, b in zip(xs, lo, hi)]).to(BF)  # noqa: E731
+    zero = [0] * len(n)
+    if sum(one):
+        sage.cache_append(c.cache, part(keys, zero, one), part(values, zero, one), c.table,
+                          torch.tensor(one, dtype=torch.int32).cuda(), cu_seqlens=c.cu(one), rope=rope)
+    q, k, v = part(queries, one, n), part(keys, one, n), part(values, one, n)
+    kv = {} if not sum(one) else dict(cu_seqlens_kv=c.cu(n), max_seqlen_kv=max(n), total_kv=sum(n))
+    out = sage.sageattn_prefill(q, k, v, c.cache, c.table, c.seq_lens, c.cu(two), max(two), rope=rope, precision=precision,
+                                **kv)
+    assert (out.float() - v.float().repeat_interleave(Hq // H, dim=1)).abs().max() <= 0.2
+    # the same, from inputs put together here: rows read from the pages, queries turned to their positions
+    pos = torch.cat([torch.arange(a, b) for a, b in zip(one, n)]).int().cuda()
+    qr, _ = sage.qk_norm_rope(q, rope=rope, positions=pos)
+    if fmt == "16bit":
+        dense = [c.at(x, n).contiguous() for x in (c.k, c.v)]
+    else:
+        dense = [torch.from_numpy(decoded(oracle_mod, c.at(x, n).cpu().numpy(), c.at(s, n).cpu().numpy())).to(BF).cuda()
+                 for x, s in ((c.k, c.ks), (c.v, c.vs))]
+    assert torch.equal(out, sage.sageattn_varlen(qr, *dense, c.cu(two), c.cu(n), max(two), max(n), is_causal=True,
+                                                 precision=precision))
 
 @pytest.mark.parametrize("fmt", ["16bit", "fp4"])
 def test_padded_prompts(sage, fmt):
