@@ -438,6 +438,23 @@ def test_fp4_every_scale_at_every_border(sage, oracle_mod, dtype):
         np.testing.assert_array_equal(c.at(codes, new).cpu().numpy(), wc)
 
 
+@pytest.mark.parametrize("dtype,inter", [(BF, False), (HF, True)])
+def test_fp4_codes_of_many_rows(sage, oracle_mod, dtype, inter):
+    """Norm, rotation and quantization of eight million key elements, codes and scales bit for bit: enough for values
+    within a step of binary32 of a border between two codes."""
+    N, H, D = 8192, 8, 128
+    c = Case(sage, [N], 64, H, D, dtype, "fp4")
+    g = gen(19)
+    k, w = randn(g, N, H, D, dtype=dtype), 1 + 0.1 * torch.randn(D, generator=g, device="cuda")
+    rope = sage.rope_table(N, D)
+    sage.cache_append(c.cache, k, k, c.table, c.seq_lens, cu_seqlens=c.cu([N]), k_weight=w, eps=EPS, rope=rope, interleaved=inter)
+    kd = rows32(k, w, rope, torch.arange(N), inter)
+    for rows, codes, sf in ((kd, c.k, c.ks), (k.float().cpu(), c.v, c.vs)):
+        wc, ws = quantized(oracle_mod, rows)
+        np.testing.assert_array_equal(c.at(sf, [N]).cpu().numpy(), ws)
+        np.testing.assert_array_equal(c.at(codes, [N]).cpu().numpy(), wc)
+
+
 @pytest.mark.parametrize("fmt", ["16bit", "fp4"])
 def test_bad_tables_are_reported_and_not_followed(sage, oracle_mod, fmt):
     lens = [20, 20, 20, 20]
