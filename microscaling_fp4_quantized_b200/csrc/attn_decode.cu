@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? (HT == 8 && D ==
   // of binary32 beyond 2^26 would carry the best key's weight out of its type).
   float o[NT][KS][4], m[NT][2], rise[NT][2], l[NT][2], qs[NT][2];
   [[maybe_unused]] float down = kShift;  // (bf16) the exponent of weights at the maximum
+  [[maybe_unused]] const float rest = t4 < 2 ? 0.0f : 1.0f;  // (HT = 4) columns of what the rounding leaves
   uint32_t slot = 0, fill = S::kStages - 1;  // stages to read and to refill
   bool first = true;
   int head0 = pc.hk * p.group + pc.chunk * p.chunk_heads, heads = min(p.chunk_heads, p.group - pc.chunk * p.chunk_heads);
@@ -743,17 +744,18 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? (HT == 8 && D ==
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[g][n][e] = ex2_approx(fmaf(s[g][n][e] - m[n][e & 1], qs[n][e & 1], kMmaBf16 ? down : kShift));
+          for (int e = 0; e < 4; ++e)
+            s[g][n][e] = ex2_approx(fmaf(s[g][n][e] - m[n][e & 1], qs[n][e & 1], kMmaBf16 ? down : kShift));
           float h[4] = {s[g][n][0], s[g][n][1], s[g][n][2], s[g][n][3]};
-          uint32_t w[2] = {pack_p<kMmaBf16>(h[0], h[1]), pack_p<kMmaBf16>(h[2], h[3])};
+          const uint32_t w[2] = {pack_p<kMmaBf16>(h[0], h[1]), pack_p<kMmaBf16>(h[2], h[3])};
+          // (HT = 4: the weight itself in columns 0 to 3, by a factor of 0)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = s[g][n][e] - h[e];
+          for (int e = 0; e < 4; ++e) h[e] = HT == 4 ? fmaf(-h[e], rest, s[g][n][e]) : s[g][n][e] - h[e];
           const uint32_t left[2] = {pack_p<kMmaBf16>(h[0], h[1]), pack_p<kMmaBf16>(h[2], h[3])};
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if constexpr (HT == 4) w[e] = t4 < 2 ? w[e] : left[e];
-            else pl[n][e] = movm_t(left[e]);
-            pb[n][e] = movm_t(w[e]);
+            pb[n][e] = movm_t(HT == 4 ? left[e] : w[e]);
+            if constexpr (HT == 8) pl[n][e] = movm_t(left[e]);
           }
           l[n][0] += s[g][n][0] + s[g][n][2];
           l[n][1] += s[g][n][1] + s[g][n][3];
