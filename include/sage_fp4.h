@@ -352,10 +352,13 @@ sage_status_t sage_fp4_set_wait_timeout_ns(uint64_t ns);
  * it back as dense tensors, and attention of one new token per sequence over it.
  *
  * Norm and rotation of one head x (D channels), in binary32 with one rounding at the end:
- *   y = x * w / sqrt(mean(x^2) + eps)                 (with weights w; the mean in binary64)
+ *   y = x * w / sqrt(mean(x^2) + eps)                 (with weights w)
  *   (y_i, y_j) -> (y_i c - y_j s, y_j c + y_i s)      (with a table) for the R / 2 pairs of
  *   the first R = rotary_dim channels: j = i + R/2, or (2i, 2i + 1) when interleaved;
  *   c = rope[pos * R + pair], s = rope[pos * R + R/2 + pair].
+ * Every product and sum of the rotation is rounded to binary32 on its own. The mean is formed in
+ * binary32 for rows that are rounded to 16 bits (in binary64 where squares leave binary32's range) and
+ * in binary64 for keys that are quantized to FP4.
  */
 typedef struct {
   const void* q_weight;   /* [D] norm weights of the query heads, or NULL: no norm */
@@ -460,8 +463,11 @@ size_t sage_fp4_decode_workspace_bytes(const sage_fp4_cache_t* cache, const sage
  * over the seq_lens[b] tokens of sequence b and the key/value head h / (Hq / Hkv). q and out are
  * [B, Hq, D] with strides of (sequence, head); out may be q (with the same strides), otherwise the
  * two must not overlap. A sequence of length 0 gets zeros, and so does a head whose scores are all
- * -inf. Small problems run in one launch, by pairs of sequence and head; else the batch's tokens are
- * cut into equal shares, whatever the lengths, and the parts of a pair joined by a second launch.
+ * -inf. Scores, their maximum, the sums and the joining of parts are binary32; weights enter the
+ * product with the values as a 16-bit value and the 16-bit remainder of its rounding (bf16 caches
+ * bf16, 2^-16 in all; fp16 and FP4 caches fp16, 2^-22). Finite values of any size and number have finite
+ * averages. Small problems run in one launch, by pairs of sequence and head; else the batch's tokens
+ * are cut into equal shares, whatever the lengths, and the parts of a pair joined by a second launch.
  * Results do not depend on timing. workspace: 256-byte aligned, at least
  * sage_fp4_decode_workspace_bytes(); calls that may overlap need one each.
  */

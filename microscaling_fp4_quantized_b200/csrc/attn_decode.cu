@@ -3,9 +3,10 @@
 //   out[b, h] = sum_n p_n v_n / sum_n p_n,  p_n = exp(sm_scale q[b, h] . k_n - m),  n < seq_lens[b]
 //
 // Bound: every cached key and value is read once for all query heads that share it, 4 D bytes a
-// token and head (FP4: 1.125 D), against 4 D flops per query head: with up to 16 query heads per
-// key/value head the tensor rate needed at the full memory rate is under a twentieth of the
-// chip's, so HBM is the floor.
+// token and head (FP4: 1.125 D), against 4 D flops per query head. 16-bit caches: with up to 16 query
+// heads per key/value head the tensor rate needed at the full memory rate is under a twentieth of the
+// chip's, so HBM is the bound. FP4 caches have the same floor, but need up to 57 flops a byte and, before
+// them, every code in fp16: their bound is the instructions below.
 //
 // Work split. The tokens of all (sequence, key/value head) pairs are cut into tiles, laid end to
 // end and dealt to the CTAs (as many as fit the machine) in contiguous shares of equal cost, so
@@ -24,12 +25,14 @@
 // the operand of O^T = V^T P^T. The running maximum is raised only when a score exceeds it by
 // 2^4, checked by one vote per tile: probabilities then reach 2^4 times the scale they are kept at.
 //
-// Measured on one B200, joins included, share of the 6549 GB/s a copy reaches: 16-bit, 16 sequences of
-// 256 to 16384 tokens, 32 heads on 8, D 128: 80.3 us, 6.28 TB/s (0.96). 16-bit, 8 sequences of 2000 to 8192,
-// 16 heads, D 64: 31.4 us, 5.34 TB/s (0.81). FP4, 64 sequences of 128 to 8192, 32 heads on 8: 78.5 us,
-// 4.16 TB/s (0.64), with D 64 50.8 us (0.49); one sequence of 131071: 40.7 us, 3.71 TB/s (0.57). FP4 is
-// bound by the instructions that decode it, about 330 per 16 keys (113 for V, 91 for K, 48 for the copies) at
-// 2.4 a cycle and SM; a second launch, the join, costs 2 to 4 us.
+// Measured on several B200s, joins included, share of the 6549 GB/s a copy reaches: 16-bit, 16 sequences of
+// 256 to 16384 tokens, 32 heads on 8, D 128: 81 to 84 us, 6.0 to 6.2 TB/s (0.92 to 0.95), 128 heads on 8 88 us.
+// 16-bit, 8 sequences of 2000 to 8192, 16 heads, D 64: 32.2 us, 5.2 TB/s (0.80). FP4, 64 sequences of 128 to
+// 8192, heads on 8: D 128 32 heads 80 to 86 us (0.58 to 0.62), 64 heads 90 (0.56), 128 heads 131 (0.38), D 64
+// 32 heads 52 us (0.48); one sequence of 131071, D 128: 41 to 42 us, 3.6 TB/s (0.56). FP4 waits for the
+// instructions that decode it, about 348 per 16 keys (331 before weights had a remainder: 113 for V, 91 for K,
+// 48 for the copies), with the 16 warps an SM that 128 registers leave: issue at 63 %, ALU at 53 %, no other
+// unit above 40 %. A second launch, the join, costs 2 to 4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -266,9 +269,10 @@ __device__ __forceinline__ void scores_fp4(const uint8_t* stage, int k0, int r, 
   }
 }
 
-// O^T += V^T (P + P_lo)^T over 16 FP4 keys (TWO; else P holds both, in columns of their own). Lane (r, t4) takes channels r D/8 .. of keys 2t, 2t+1, 2t+8, 2t+9;
-// the operand wants two keys' values of one channel side by side, so the nibbles of two
-// keys are interleaved before they are decoded.
+// O^T += V^T P^T over 16 FP4 keys, with TWO also that of pl, what the rounding of the weights left (else
+// P holds both, in columns of their own). Lane (r, t4) takes channels r D/8 .. of keys 2t, 2t+1, 2t+8,
+// 2t+9; the operand wants two keys' values of one channel side by side, so the nibbles of two keys are
+// interleaved before they are decoded.
 template <int D, int NT, bool TWO>
 __device__ __forceinline__ void values_fp4(const uint8_t* stage, int k0, int r, int t4, const uint32_t (&pb)[NT][2],
                                            const uint32_t (&pl)[NT][2], float (&o)[NT][D / 16][4]) {
@@ -737,8 +741,9 @@ __global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : FP4 ? (HT == 8 && D ==
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        // Weights as operands: the rounded weight and, in an operand or columns of its own, what the rounding left. One
-        // rounding alone would be as large as the output's (of bf16; of fp16 on FP4 caches).
+        // Weights as operands: the rounded weight and, in an operand or columns of its own, what the rounding left,
+        // rounded in turn (2^-16 of the weight in bf16, 2^-22 in fp16). One rounding alone would be as large as the
+        // output's (of bf16; of fp16 on FP4 caches).
         uint32_t pb[NT][2];
         [[maybe_unused]] uint32_t pl[NT][2];
 #pragma unroll
@@ -1088,7 +1093,7 @@ cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   // shares (us, sequences x tokens, 32 heads on 8, D 128): 16-bit, 1 x 64 3.7 / 4.6, 1 x 1024 6.8 / 6.9,
   // 1 x 4096 11.3 / 9.3, 4 x 2048 9.8 / 10.7, 16 x 512 8.9 / 11.2, 16 x 1024 16.4 / 18.3, 16 x 1024 to 8192
   // 63 / 48, 64 x 512 27.2 / 29.7, 200 x 64 22.5 / 19.4; FP4, 1 x 1024 6.7 / 7.8, 16 x 4096 24.3 / 26.8,
-  // 64 x 1024 23.0 / 28.7, 64 x 256 to 2048 35.0 / 32.4, 200 x 512 34.4 / 42.6.
+  // 64 x 1024 23.0 / 28.7, 64 x 256 to 2048 35.0 / 32.4, 200 x 512 34.4 / 42.6 (when chosen).
   const int per = (tiles + cluster - 1) / cluster;
   if (pairs <= 3 * static_cast<int64_t>(fit) && per <= 8 && per <= pairs * (tiles + 1) / fit + 3) {
     resident_ctas<decode_kernel<T, D, NT, HT, FP4, true>>(smem, &e);
@@ -1104,10 +1109,12 @@ cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   // a token's rows of all heads (adjacent in NHD order, where a head's 32 bytes of codes and 4 of scales are
   // parts of the DRAM's and L2's units) and the page table are fetched once. It needs a multiple of HC blocks, and the
   // rest of the machine stays idle: up to an eighth of it in NHD order, almost nothing otherwise. Measured by
-  // all heads' tiles end to end / side by side (us): FP4 D = 64, 10 sequences of 24078 to 78702 tokens, 56 heads on 8,
-  // NHD 211 / 99.7 (end to end it read 3.9 times its bytes from DRAM), HND 98.5 / 97.4; the same with D = 128 NHD
-  // 269 / 156; 16 sequences of 256 to 16384, 32 heads on 8: FP4 D = 128 NHD 46.3 / 41.9, HND 40.9 / 39.9, 16-bit
-  // D = 64 NHD 46.9 / 43.8, HND 43.6 / 43.1, D = 128 NHD 81.0 / 79.8, HND 82.0 / 80.5.
+  // all heads' tiles end to end / side by side (us): FP4, 10 sequences of 24078 to 78702 tokens, 56 heads on 8, D = 64
+  // NHD 218.6 / 109.7 (end to end it read 3.9 times its bytes from DRAM), HND 109.6 / 107.6, D = 128 NHD 231 / 177,
+  // HND 165.4 / 166.9; 16 sequences of 256 to 16384, 32 heads on 8: FP4 D = 64 NHD 34.7 / 30.1, HND 28.0 / 27.5,
+  // D = 128 NHD 47.2 / 43.0, HND 41.0 / 40.3, 16-bit D = 64 NHD 48.9 / 44.3, HND 44.7 / 43.7, D = 128 NHD 82.3 /
+  // 80.9, HND 84.4 / 81.6. It loses a little where head-major pages share nothing and the shares come out less even:
+  // besides the D = 128 HND case above, 16-bit, 16 sequences of 128 to 8192, 64 heads on 4, HND 34.3 / 35.2.
   const bool nhd = p.c.sk.h < p.c.sk.n && p.c.sv.h < p.c.sv.n;
   if (groups * HC * 64 >= p.grid * (nhd ? 56 : 63)) {
     p.side = HC;
@@ -1120,9 +1127,10 @@ cudaError_t launch_one(DecodeParams p, int max_grid, cudaStream_t stream) {
   return launch_dependent(join_kernel<T, D, NT>, dim3(p.joins, p.chunk_heads), few ? 16 * kMaxGroups : 128, 0, stream, p);
 }
 
-// FP4 caches with at most four heads a chunk: every head in two columns, so that the remainders of the weights cost no
-// product of their own. Measured, two columns / two products (us): FP4, 64 sequences of 128 to 8192 tokens, 32 heads on
-// 8, D 128 80.7 / 88.1, D 64 51.7 / 55.9; one sequence of 131071 41.2 / 45.1. 16-bit caches are not bound by the products.
+// FP4 caches with at most four heads a chunk: every head in two columns, so that the remainders of the weights
+// cost no product of their own. Measured, two columns / two products (us): FP4, 64 sequences of 128 to 8192
+// tokens, 32 heads on 8, D 128 80.0 / 88.1, D 64 52.0 / 55.9; one sequence of 131071 41.2 / 45.1. 16-bit caches
+// are not bound by the products.
 template <typename T, int D>
 cudaError_t launch_format(const DecodeParams& p, bool fp4, int NT, int max_grid, cudaStream_t stream) {
   if (!fp4)

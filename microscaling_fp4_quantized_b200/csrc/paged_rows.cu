@@ -5,12 +5,14 @@
 // apart as the two halves of a rotation pair (i, i + R/2): neither pairing needs a shuffle, and
 // neighbouring lanes move neighbouring chunks; only the mean square and the FP4 block maximum cross
 // lanes. A lane group keeps its token's cosines, sines and norm weights in registers over the heads of its
-// item; the arithmetic runs on two channels per instruction. All three operations are bound by HBM: each
-// row is read once and written once. Measured on one B200, share of the 6549 GB/s a copy
-// reaches: norm and rotation of B1 H24 N32768 D128 143 us, 5.73 TB/s (0.88); prompt of 8191 tokens, 32 + 8
-// heads, 31.3 us, 5.42 TB/s (0.83); append of 17,995 tokens, 32 query and 8 key/value heads, 92 us, 4.8 TB/s
-// (0.73), to FP4 pages 88.5 us, 4.4 TB/s (0.67: the encoding's instructions); dense read of 131,481 cached FP4
-// tokens, 8 heads, 106 us, 6.08 TB/s (0.93).
+// item; the arithmetic runs on two channels per instruction. Each row is read once and written once: the
+// floor of all three is HBM. Measured on several B200s, share of the 6549 GB/s a copy reaches: norm and
+// rotation of B1 H24 N32768 D128 144 to 148 us, 5.6 to 5.7 TB/s (0.85 to 0.87); prompt of 8191 tokens, 32 + 8
+// heads, 31.4 us, 5.4 TB/s (0.83); dense read of 123,171 cached FP4 tokens, 8 heads, 107 us, 6.04 TB/s (0.92).
+// Append of 17,823 tokens, 8 key/value heads, 16-bit 30.3 us (0.74), FP4 41.3 us (0.35), with 32 query heads
+// 90.5 (0.74) and 87.7 (0.67): nothing is saturated there (issue at 34 % and 47 %, ALU 25 % and 33 %). 128
+// registers leave 16 warps an SM (19 % of its warps active) to hide a chain of loads to a token's place, the
+// rows' own latency and, for FP4, the reductions and conversions of the encoding.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -205,7 +207,7 @@ __device__ __forceinline__ Place place_of(const CacheView& c, int tok, bool lead
 // Rows in flight per lane group: four loaded together, or two with the next two already on their way
 // where the arithmetic of quantization has to be hidden. Measured (us, 128 registers, 16 warps an
 // SM): norm and interleaved rotation of B1 H24 N32768 D128 143 against 143, prompt of 8191 tokens with 32 + 8
-// heads 31.8 against 35.6, append of 17,995 tokens to an FP4 cache and its read 131 against 115 (when chosen). Three
+// heads 31.8 against 35.6, append of 17,823 tokens to an FP4 cache and its read 131 against 115 (when chosen). Three
 // blocks' worth of registers (80) spill and lose a quarter; 8 channels a lane need as many instructions
 // for half the bytes and lose 40 %.
 template <typename T, int D, bool CACHE, bool FP4, bool INTER>
@@ -529,7 +531,7 @@ static cudaError_t rows_of_type(const RowsParams& p, int D, bool to_cache, bool 
 
 // Heads a warp walks: as many as leave `waves` times the warps that are resident (148 SMs of 16), at
 // most 16. Dense rows: four times (with one, the prompt above takes 32.7 us instead of 31.3). Paged ones: once, as
-// finding a token's place is a chain of loads (with four, keys and values of 17,995 tokens, 8 heads, take 48.4 us
+// finding a token's place is a chain of loads (with four, keys and values of 17,823 tokens, 8 heads, took 48.4 us
 // instead of 41.5 to FP4 pages and 35.1 instead of 31.8 to 16-bit ones).
 static int heads_of(int64_t groups, int heads, int waves) {
   int n = 16;
