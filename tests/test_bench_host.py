@@ -49,6 +49,13 @@ def test_traffic_reported_while_sources_match(bench_mod, tmp_path, monkeypatch):
     assert t3 is None and "changed" in src3
 
 
+def test_the_committed_record_belongs_to_the_committed_sources(bench_mod):
+    """Otherwise the bench line has no traffic: a change of one of these files needs the capture again."""
+    from microscaling_fp4_quantized_b200 import workloads as W
+    t, src = bench_mod._attn_traffic(W.LONG)
+    assert t is not None and W.PROFILE.name in src, src
+
+
 def test_traffic_absent_record(bench_mod, tmp_path, monkeypatch):
     from microscaling_fp4_quantized_b200 import workloads as W
     monkeypatch.setattr(bench_mod, "ROOT", str(tmp_path))
